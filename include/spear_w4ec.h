@@ -135,6 +135,79 @@ int spear_w4ec_import(spear_w4ec *h, const void *codes, const float *s, const ui
 int spear_w4ec_forward(const spear_w4ec *h, const void *x, void *y, int64_t M,
                        uint32_t flags, void *stream);
 
+/* ---- Operators around the layer: the norm in front of it, activations in
+ * 8 bits, and what follows the product in the same kernel.  (SPEAR's pages
+ * describe none of them; they are what a serving step of a transformer needs
+ * between one W4 layer and the next.) */
+
+/* Activations of an epilogue, in fp32. */
+enum {
+    SPEAR_ACT_NONE = 0,
+    SPEAR_ACT_RELU = 1,
+    SPEAR_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
+    SPEAR_ACT_GELU = 3,      /* v (1 + erf(v / sqrt 2)) / 2 */
+    SPEAR_ACT_GELU_TANH = 4  /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+};
+
+/* Epilogue of a forward call:  y = act(Y + bias) * mul + residual, with Y the
+ * layer's output (W4 product and Error Compensator) in fp32 and one rounding
+ * to bf16 at the end.  NULL leaves a term out.  All pointers are 16-byte
+ * aligned device memory that may have been written by earlier work on the
+ * stream. */
+typedef struct spear_w4ec_epilogue {
+    const void *bias;      /* dev bf16 [N] */
+    const void *mul;       /* dev bf16 [M][N]: e.g. the activated gate projection of a gated MLP */
+    const void *residual;  /* dev bf16 [M][N] */
+    int32_t act;           /* SPEAR_ACT_* */
+    int32_t reserved;      /* 0 */
+} spear_w4ec_epilogue;
+
+/* spear_w4ec_forward with an epilogue (ep = NULL: none, the result then equals
+ * spear_w4ec_forward's with SPEAR_FORCE_FUSED).  mul and residual may each be
+ * y itself (in-place residual addition); every other overlap of y with an
+ * operand is SPEAR_ERR_INVALID.  flags: as spear_w4ec_forward, except that the
+ * EC is always formed in the kernel of the product: SPEAR_FORCE_SPLIT is
+ * SPEAR_ERR_UNSUPPORTED, and a tuned table's path is followed without its
+ * placement. */
+int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M, const spear_w4ec_epilogue *ep,
+                          uint32_t flags, void *stream);
+
+/* The same on 8-bit activations:  x[t,k] = xs[t] * xq[t,k].
+ *   xq  dev e4m3 [M][K] (4 exponent bits of bias 7, 3 mantissa bits, no
+ *       infinities, 0x7F and 0xFF NaN), 16-byte aligned
+ *   xs  dev float [M]: one scale a token
+ * The products x (q - z) are exact and summed in fp32; a token with a NaN
+ * code, or whose scale is not finite, has NaN or infinite outputs.  ep may be
+ * NULL.  The dispatch table is not used: SPEAR_FORCE_DECODE and SPEAR_FORCE_TC
+ * pick a kernel family as in spear_w4ec_forward. */
+int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y, int64_t M,
+                          const spear_w4ec_epilogue *ep, uint32_t flags, void *stream);
+
+/* Root-mean-square norm of M rows of K elements, with the residual's addition
+ * in front and the result in bf16, in 8 bits with one scale a row, or both:
+ *   h[t,k] = bf16(x[t,k] + residual[t,k])          (h = x if residual is NULL)
+ *   v[t,k] = h[t,k] * weight[k] / sqrt(mean_k h[t,k]^2 + eps)
+ *   y[t,k] = bf16(v[t,k])
+ *   s[t]   = a_t / 448,  q[t,k] = e4m3(v[t,k] * (448 / a_t)),
+ *            a_t = max(max_k |v[t,k]|, 2^-100)
+ * in fp32, each output rounded once (to nearest even).  (q, s) is what
+ * spear_w4ec_forward_q8 takes.  A row with an infinity or NaN has a scale that
+ * is not finite, or NaN outputs.
+ *   x, residual, sum, y   dev bf16 [M][K]   weight  dev bf16 [K]
+ *   q  dev e4m3 [M][K]    s  dev float [M]
+ * residual and sum (h) are both given or both NULL; y or (q and s) is given;
+ * all but s are 16-byte aligned.  sum and y may each be x or residual itself,
+ * but no output may overlap another buffer otherwise (SPEAR_ERR_INVALID).
+ * Any 1 <= K < 2^31 and 0 <= M < 2^31 (M = 0 is a no-op); rows whose K is a
+ * multiple of 8 are the fast case.  0 <= eps < 1e30.  Runs on the current
+ * device and `stream`; no handle, no allocation, no scratch. */
+int spear_w4ec_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int64_t M, int64_t K,
+                       void *sum, void *y, void *q, float *s, void *stream);
+
+/* 8-bit quantisation alone: q and s of x's own rows, as in spear_w4ec_rmsnorm
+ * with v = x (an all-zero row has q = 0 and s = 2^-100 / 448). */
+int spear_w4ec_quantize_q8(const void *x, int64_t M, int64_t K, void *q, float *s, void *stream);
+
 /* The same as spear_w4ec_forward, with x and y in HOST memory: copies x to a
  * device staging buffer, runs the forward and copies y back, all on `stream`,
  * then synchronises the stream.  Pinned host memory gives the fastest copies.

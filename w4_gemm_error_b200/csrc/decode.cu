@@ -51,6 +51,7 @@
 #include <vector>
 
 #include "async_utils.cuh"
+#include "epilogue.cuh"
 #include "kernels.h"
 #include "tensor_map.h"
 
@@ -97,11 +98,12 @@ struct DecodeParams {
     float b_g;
     const void *pf;       // codes of the next layer, prefetched into L2 (null for none)
     uint64_t pf_bytes;
+    Epilogue epi;         // forms kEpi and kQ8
 };
 
 // Bytes of one ring stage: the codes of 64 rows x 256 k (or 16 G rows x
 // 256 k as four 2 KB boxes), then the activations as four 64-k sub-tiles of
-// TOK rows x 128 bytes.
+// TOK rows x 128 bytes (form kQ8: 64 bytes, in the same space).
 template <int TOK>
 __host__ __device__ constexpr uint32_t stage_bytes()
 {
@@ -145,10 +147,39 @@ __device__ __forceinline__ bool wait_u_published(const DecodeParams &p, unsigned
     return true;
 }
 
+// The 16 activations k = 16 cl .. + 15 of row t of a 64-k sub-tile as the
+// pairs that enter the MMA.  Form kQ8: 64-byte rows of e4m3 with the 64B
+// swizzle, made f16 (beside the weights' integers) or bf16 (beside rows of
+// G), both exact.
+template <int FORM>
+__device__ __forceinline__ void read_x16(const uint8_t *xt, int t, int cl, bool is_u, uint4 (&v)[2])
+{
+    if constexpr (FORM == kQ8) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(xt + t * 64 + ((cl ^ ((t >> 1) & 3)) << 4));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = e4m3x2_to_f16x2((uint16_t)w[i]);
+            o[2 * i + 1] = e4m3x2_to_f16x2((uint16_t)(w[i] >> 16));
+        }
+        if (is_u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] = f16x2_to_bf16x2(o[i]);
+        v[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        v[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    } else {
+        v[0] = *reinterpret_cast<const uint4 *>(xt + t * 128 + (((2 * cl) ^ (t & 7)) << 4));
+        v[1] = *reinterpret_cast<const uint4 *>(xt + t * 128 + (((2 * cl + 1) ^ (t & 7)) << 4));
+    }
+}
+
 // Register budget: with 16 consumer warps two CTAs per SM; with 8, three
 // CTAs per SM up to 16 tokens (the grid is about two per SM, and the next
 // layer's kernel starts beside it) and two at 32 tokens.
-template <int T, int W>
+// FORM: see epilogue.cuh.
+template <int T, int W, int FORM>
 __global__ void __launch_bounds__(block_threads(W), (W == 16 || T == 4) ? 2 : 3)
 decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_g,
                    const __grid_constant__ CUtensorMap tm_bt, const __grid_constant__ CUtensorMap tm_x,
@@ -160,7 +191,8 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
     constexpr int kProducerWarp = W;
     constexpr int KPAR = W / 4;      // consumer warps per 16-row group
     constexpr uint32_t kStage = stage_bytes<TOK>();
-    constexpr uint32_t kXBytes = 4 * TOK * 128;
+    constexpr int kXTile = TOK * (FORM == kQ8 ? 64 : 128);   // bytes of a 64-k sub-tile of activations
+    constexpr uint32_t kXBytes = 4 * kXTile;
     extern __shared__ uint8_t smem_raw[];
     // per stage: codes landed, activations landed, stage free; then B^T, K-split receive
     __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 2];
@@ -224,7 +256,7 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             tma_load_3d(dst, &tm_x, 0, 0, (k0 + c * kChunk) / 64, bar);
         else
             for (int i = 0; i < 4; ++i)
-                tma_load_2d(dst + i * (TOK * 128), &tm_x, k0 + c * kChunk + 64 * i, 0, bar);
+                tma_load_2d(dst + i * kXTile, &tm_x, k0 + c * kChunk + 64 * i, 0, bar);
     };
 
     if (producer && lane == 0) {
@@ -350,9 +382,7 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         // ---- 64 weight rows: warp w owns rows 16(w mod 4) .. +15 and the sub-blocks
         // sb = w/4 (mod KPAR) of each stage
         const int kq = warp >> 2;
-        const uint32_t nbg = __bfloat16_as_ushort(__float2bfloat16_rn(-(float)(128u + zg_raw)));
-        const uint32_t nbh = __bfloat16_as_ushort(__float2bfloat16_rn(-(float)(128u + zh_raw)));
-        const uint32_t negg = nbg | (nbg << 16), negh = nbh | (nbh << 16);
+        const uint32_t negg = dequant_bias<FORM == kQ8>(zg_raw), negh = dequant_bias<FORM == kQ8>(zh_raw);
         int s = 0;
         uint32_t par = 0;
         for (int c = 0; c < nch && ok; ++c) {
@@ -367,29 +397,26 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 const int chunk = ((2 * sb + (cl >> 1)) ^ (rg & 7)) * 16 + (cl & 1) * 8;
                 const uint2 wgv = *reinterpret_cast<const uint2 *>(ctile + rg * 128 + chunk);
                 const uint2 whv = *reinterpret_cast<const uint2 *>(ctile + (rg + 8) * 128 + chunk);
-                const uint8_t *xt = ctile + 8192 + sb * (TOK * 128);
+                const uint8_t *xt = ctile + 8192 + sb * kXTile;
                 uint4 xv[T][2];
 #pragma unroll
-                for (int n = 0; n < T; ++n) {
-                    const int t = 8 * n + gid;
-                    xv[n][0] = *reinterpret_cast<const uint4 *>(xt + t * 128 + (((2 * cl) ^ (t & 7)) << 4));
-                    xv[n][1] = *reinterpret_cast<const uint4 *>(xt + t * 128 + (((2 * cl + 1) ^ (t & 7)) << 4));
-                }
+                for (int n = 0; n < T; ++n)
+                    read_x16<FORM>(xt, 8 * n + gid, cl, false, xv[n]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t wgw = j ? wgv.y : wgv.x, whw = j ? whv.y : whv.x;
                     // codes k = 8j + {0..7}: nibbles (m, m + 4) hold the pair k = 2m, 2m + 1,
                     // the order of the activations in v
-                    const uint32_t g0 = dequant_pair(wgw, negg), g1 = dequant_pair(wgw >> 4, negg);
-                    const uint32_t g2 = dequant_pair(wgw >> 8, negg), g3 = dequant_pair(wgw >> 12, negg);
-                    const uint32_t h0 = dequant_pair(whw, negh), h1 = dequant_pair(whw >> 4, negh);
-                    const uint32_t h2 = dequant_pair(whw >> 8, negh), h3 = dequant_pair(whw >> 12, negh);
+                    const uint32_t g0 = dequant<FORM == kQ8>(wgw, negg), g1 = dequant<FORM == kQ8>(wgw >> 4, negg);
+                    const uint32_t g2 = dequant<FORM == kQ8>(wgw >> 8, negg), g3 = dequant<FORM == kQ8>(wgw >> 12, negg);
+                    const uint32_t h0 = dequant<FORM == kQ8>(whw, negh), h1 = dequant<FORM == kQ8>(whw >> 4, negh);
+                    const uint32_t h2 = dequant<FORM == kQ8>(whw >> 8, negh), h3 = dequant<FORM == kQ8>(whw >> 12, negh);
 #pragma unroll
                     for (int n = 0; n < T; ++n) {
                         const uint4 v = xv[n][j];
                         float (&a)[4] = j ? acc2[n] : acc[n];
-                        mma_bf16_16816(a, g0, h0, g1, h1, v.x, v.y);
-                        mma_bf16_16816(a, g2, h2, g3, h3, v.z, v.w);
+                        mma_16816<FORM == kQ8>(a, g0, h0, g1, h1, v.x, v.y);
+                        mma_16816<FORM == kQ8>(a, g2, h2, g3, h3, v.z, v.w);
                     }
                 }
             }
@@ -429,7 +456,7 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 if ((4 * c + j) % W != warp)
                     continue;
                 const uint8_t *gt = stage + j * 2048;
-                const uint8_t *xt = stage + 8192 + j * (TOK * 128);
+                const uint8_t *xt = stage + 8192 + j * kXTile;
                 const int ra = gid, rb = gid + 8;
                 const uint4 a0 = *reinterpret_cast<const uint4 *>(gt + ra * 128 + (((2 * cl) ^ (ra & 7)) << 4));
                 const uint4 a1 = *reinterpret_cast<const uint4 *>(gt + ra * 128 + (((2 * cl + 1) ^ (ra & 7)) << 4));
@@ -439,10 +466,10 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 const uint32_t ha[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
                 for (int n = 0; n < T; ++n) {
-                    const int t = 8 * n + gid;
-                    const uint4 x0 = *reinterpret_cast<const uint4 *>(xt + t * 128 + (((2 * cl) ^ (t & 7)) << 4));
-                    const uint4 x1 = *reinterpret_cast<const uint4 *>(xt + t * 128 + (((2 * cl + 1) ^ (t & 7)) << 4));
-                    const uint32_t xa[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                    uint4 xv[2];
+                    read_x16<FORM>(xt, 8 * n + gid, cl, true, xv);
+                    const uint32_t xa[8] = {xv[0].x, xv[0].y, xv[0].z, xv[0].w,
+                                            xv[1].x, xv[1].y, xv[1].z, xv[1].w};
                     // natural pairs: step s covers k = 16 cl + 4s + {0,1} and + {2,3}
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -564,6 +591,25 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         return;
     }
 
+    // epilogue operands of this thread's outputs (row tid mod 64, tokens tid / 64 +
+    // kPh i), in flight while the K split is summed
+    constexpr int kPh = kConsumers / 64;
+    constexpr int kTokPerThread = TOK / kPh;
+    EpiOperands eo[FORM == kPlain ? 1 : kTokPerThread];
+    float xs_epi[FORM == kQ8 ? kTokPerThread : 1];
+    if constexpr (FORM != kPlain) {
+        const int64_t n = n0 + (tid & (kRows - 1));
+#pragma unroll
+        for (int i = 0; i < kTokPerThread; ++i) {
+            const int t = (tid >> 6) + kPh * i;
+            const bool mine = rank == 0 && tid < kConsumers && t < p.M;
+            if (mine && n < p.N)
+                eo[i] = epi_load(p.epi, t, n, p.N);
+            if constexpr (FORM == kQ8)
+                xs_epi[i] = mine ? __ldg(p.epi.xs + t) : 0.f;
+        }
+    }
+
     // ---- sum the K split over the cluster, in rank order, in the first CTA.
     // With an EC, u is published by the EC CTAs as ES x CS partials (one per
     // slice of K), which are summed (slice order) into u0 [TOK] (gate logits)
@@ -653,8 +699,6 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
 
     // ---- epilogue of a 64-row cluster: consumer thread = row (tid mod 64) and
     // the tokens th + kPh * i, th = tid / 64
-    constexpr int kPh = kConsumers / 64;
-    constexpr int kTokPerThread = TOK / kPh;
     if (tid < kConsumers) {
         if (p.JB > 0 && !wait_bounded(bar_bt, 0))
             atomicOr(p.status, kStatusTimeout);
@@ -693,13 +737,19 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             }
 #pragma unroll
             for (int i = 0; i < kTokPerThread; ++i) {
-                const float g = 1.0f / (1.0f + expf(-(u0[th + kPh * i] + p.b_g)));
+                // (form kQ8: u is that of the 8-bit values, xs_epi times it the layer's)
+                const float u_gate = FORM == kQ8 ? xs_epi[i] * u0[th + kPh * i] : u0[th + kPh * i];
+                const float g = 1.0f / (1.0f + expf(-(u_gate + p.b_g)));
                 out[i] += g * corr[i];
             }
         }
 #pragma unroll
         for (int i = 0; i < kTokPerThread; ++i) {
             const int t = th + kPh * i;
+            if constexpr (FORM == kQ8)
+                out[i] *= xs_epi[i];
+            if constexpr (FORM != kPlain)
+                out[i] = epi_apply(p.epi, out[i], eo[i]);
             if (t < p.M && n < p.N)
                 p.y[(int64_t)t * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(out[i]));
         }
@@ -764,10 +814,22 @@ Plan plan_for(int nch, int rp, int CS, int W)
 // overhead is shared by two sub-blocks.
 int pick_warps(int T, int nch) { return (T == 1 && nch <= 4) ? 16 : 8; }
 
-template <int T, int W>
-const void *kernel_ptr()
+using DecodeFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, DecodeParams, int);
+
+// The kernel for T token groups and W consumer warps in a form.
+template <int FORM>
+DecodeFn decode_fn_of(int T, int W)
 {
-    return reinterpret_cast<const void *>(decode_w4ec_kernel<T, W>);
+    switch (T) {
+    case 1: return W == 16 ? decode_w4ec_kernel<1, 16, FORM> : decode_w4ec_kernel<1, 8, FORM>;
+    case 2: return decode_w4ec_kernel<2, 8, FORM>;
+    default: return decode_w4ec_kernel<4, 8, FORM>;
+    }
+}
+
+DecodeFn decode_fn(int T, int W, int form)
+{
+    return form == kQ8 ? decode_fn_of<kQ8>(T, W) : (form == kEpi ? decode_fn_of<kEpi>(T, W) : decode_fn_of<kPlain>(T, W));
 }
 
 }  // namespace
@@ -899,18 +961,26 @@ size_t decode_u_floats(const Packed &pk) { return (size_t)(kUFinal + 1) * pk.R1p
 cudaError_t launch_decode(const Packed &pk, const void *x, void *y, int64_t M, bool ec, const DecodeWork &w,
                           int *status, cudaStream_t st, int num_sms)
 {
+    return launch_decode_form(pk, x, pk.K, y, M, ec, w, status, st, num_sms, kPlain, Epilogue());
+}
+
+cudaError_t launch_decode_form(const Packed &pk, const void *x, int64_t ldx, void *y, int64_t M, bool ec,
+                               const DecodeWork &w, int *status, cudaStream_t st, int num_sms, int form,
+                               const Epilogue &epi)
+{
     if (M <= 0)
         return cudaSuccess;
     if (M > kDecodeMaxTokens || !w.maps)
         return cudaErrorInvalidValue;
     const Maps *m = static_cast<const Maps *>(w.maps);
     // up to 16 tokens: K split over a cluster, each CTA with its slice of x
-    if (m->stream && decode_stream_enabled() && decode_stream_fits(pk, M, num_sms))
+    if (form == kPlain && m->stream && decode_stream_enabled() && decode_stream_fits(pk, M, num_sms))
         return launch_decode_stream(pk, m->stream, x, y, M, ec, w, status, st, num_sms);
     // up to 16 tokens on a layer whose 16-row slices fit in shared memory: one
     // CTA per 16 rows over the whole of K, no exchange between CTAs
-    if (m->rows && decode_rows_fits(pk, M, num_sms))
-        return launch_decode_rows(pk, m->rows, x, y, M, ec, w, status, st, num_sms);
+    // (K a multiple of 64 there, so that 8-bit rows have no padding)
+    if (m->rows && decode_rows_fits(pk, M, num_sms, form))
+        return launch_decode_rows(pk, m->rows, x, y, M, ec, w, status, st, num_sms, form, epi);
     const bool use_ec = ec && pk.r > 0;
     DecodeParams p;
     p.Bt = pk.Bt;
@@ -933,23 +1003,30 @@ cudaError_t launch_decode(const Packed &pk, const void *x, void *y, int64_t M, b
     p.b_g = pk.b_g;
     p.pf = w.pf;
     p.pf_bytes = w.pf_bytes;
+    p.epi = epi;
     const int T = M <= 8 ? 1 : (M <= 16 ? 2 : 4);
     // the activations of one stage (TOK rows x 256 k) as one box of the view
     // [k block][token][64 k] when K is a multiple of 64 (then no box reads past
     // the end of a row), else as four 2-D boxes with k >= K filled with zeros
+    const uint32_t x_elem = form == kQ8 ? 1u : 2u;
+    const CUtensorMapDataType x_type = form == kQ8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle x_swizzle = form == kQ8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap tm_x;
     cudaError_t e = cudaErrorInvalidValue;
     p.x3 = 0;
     if (pk.K % 64 == 0) {
         const uint64_t xd[3] = {64, (uint64_t)M, (uint64_t)(pk.K / 64)};
-        const uint64_t xs[2] = {(uint64_t)pk.K * 2, 128};
+        const uint64_t xs[2] = {(uint64_t)ldx * x_elem, 64u * x_elem};
         const uint32_t xb[3] = {64, (uint32_t)(8 * T), 4};
-        e = make_map_nd(&tm_x, x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
+        e = make_map_nd(&tm_x, x, x_type, 3, xd, xs, xb, x_swizzle);
         p.x3 = e == cudaSuccess ? 1 : 0;
     }
-    if (e != cudaSuccess)
-        e = make_map(&tm_x, x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)pk.K, (uint64_t)M, 64,
-                     (uint32_t)(8 * T), CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) {
+        const uint64_t xd[2] = {(uint64_t)pk.K, (uint64_t)M};
+        const uint64_t xs[1] = {(uint64_t)ldx * x_elem};
+        const uint32_t xb[2] = {64, (uint32_t)(8 * T)};
+        e = make_map_nd(&tm_x, x, x_type, 2, xd, xs, xb, x_swizzle);
+    }
     if (e != cudaSuccess)
         return e;
     p.g3 = m->g3;
@@ -957,7 +1034,7 @@ cudaError_t launch_decode(const Packed &pk, const void *x, void *y, int64_t M, b
     // clusters then wait, bounded, for the EC clusters' partials of u)
     int CS = 0, W = 0;
     Plan pl{};
-    const void *fn = nullptr;
+    DecodeFn kernel = nullptr;
     for (int max_cs = 8; max_cs >= 1;) {
         int KS = 0;
         CS = pick_cluster(pk, num_sms, JG, &KS, max_cs);
@@ -991,8 +1068,8 @@ cudaError_t launch_decode(const Packed &pk, const void *x, void *y, int64_t M, b
                     : (T == 2 ? plan_for<16>(p.nch, p.rp, CS, W) : plan_for<32>(p.nch, p.rp, CS, W));
         if (pl.smem > 227 * 1024)
             return cudaErrorInvalidValue;
-        fn = T == 1 ? (W == 16 ? kernel_ptr<1, 16>() : kernel_ptr<1, 8>())
-                    : (T == 2 ? kernel_ptr<2, 8>() : kernel_ptr<4, 8>());
+        kernel = decode_fn(T, W, form);
+        const void *fn = reinterpret_cast<const void *>(kernel);
         e = raise_smem_limit(fn, pl.smem);
         if (e != cudaSuccess)
             return e;
@@ -1019,14 +1096,7 @@ cudaError_t launch_decode(const Packed &pk, const void *x, void *y, int64_t M, b
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    switch (T) {
-    case 1:
-        if (W == 16)
-            return cudaLaunchKernelEx(&cfg, decode_w4ec_kernel<1, 16>, m->codes, m->g, m->bt, tm_x, p, CS);
-        return cudaLaunchKernelEx(&cfg, decode_w4ec_kernel<1, 8>, m->codes, m->g, m->bt, tm_x, p, CS);
-    case 2: return cudaLaunchKernelEx(&cfg, decode_w4ec_kernel<2, 8>, m->codes, m->g, m->bt, tm_x, p, CS);
-    default: return cudaLaunchKernelEx(&cfg, decode_w4ec_kernel<4, 8>, m->codes, m->g, m->bt, tm_x, p, CS);
-    }
+    return cudaLaunchKernelEx(&cfg, kernel, m->codes, m->g, m->bt, tm_x, p, CS);
 }
 
 }  // namespace spear

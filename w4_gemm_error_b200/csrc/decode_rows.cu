@@ -32,6 +32,7 @@
 #include <new>
 
 #include "async_utils.cuh"
+#include "epilogue.cuh"
 #include "kernels.h"
 #include "tensor_map.h"
 
@@ -53,7 +54,7 @@ struct RowsMaps {
 };
 
 struct RowsParams {
-    const uint16_t *x;
+    const void *x;        // bf16 [M][K]; form kQ8: e4m3 [M][K]
     const uint16_t *Bt;   // [Np][rp]
     const float *s;
     const uint8_t *z;
@@ -73,6 +74,7 @@ struct RowsParams {
     float b_g;
     const void *pf;       // codes of the next layer, prefetched into L2 (null for none)
     uint64_t pf_bytes;
+    Epilogue epi;         // forms kEpi and kQ8
 };
 
 __device__ __forceinline__ void named_bar_sync(int id, int n)
@@ -103,8 +105,27 @@ __host__ __device__ constexpr uint32_t rows_tail_bytes(int W, int rp)
     return (uint32_t)(W * TOK * kRowsPerCta * 4 + 32 * rp + 4 * TOK * (1 + rp));
 }
 
-// Register budget: MINB CTAs per SM.
-template <int T, int W, int MINB>
+// Eight consecutive activations as the pairs that enter the MMA.  e4m3 (form
+// kQ8) becomes f16 for the row CTAs, whose weights are small integers, and
+// bf16 for the CTAs of u, whose G rows are bf16; both conversions are exact,
+// so the products are those of the 8-bit values themselves.
+template <int FORM>
+__device__ __forceinline__ uint4 load_x8(const void *x, int64_t i, bool is_u)
+{
+    if constexpr (FORM == kQ8) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(x) + i));
+        uint4 v = make_uint4(e4m3x2_to_f16x2((uint16_t)q.x), e4m3x2_to_f16x2((uint16_t)(q.x >> 16)),
+                             e4m3x2_to_f16x2((uint16_t)q.y), e4m3x2_to_f16x2((uint16_t)(q.y >> 16)));
+        if (is_u)
+            v = make_uint4(f16x2_to_bf16x2(v.x), f16x2_to_bf16x2(v.y), f16x2_to_bf16x2(v.z), f16x2_to_bf16x2(v.w));
+        return v;
+    } else {
+        return ld_nc(static_cast<const uint16_t *>(x) + i);
+    }
+}
+
+// Register budget: MINB CTAs per SM.  FORM: see epilogue.cuh.
+template <int T, int W, int MINB, int FORM>
 __global__ void __launch_bounds__(32 * W + 32, MINB)
 decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_g,
                    RowsParams p)
@@ -170,10 +191,8 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         float s_epi = 0.f;
         if (!is_u) {
             const uint32_t zg = __ldg(p.z + n0 + gid), zh = __ldg(p.z + n0 + gid + 8);
-            const uint32_t nbg = __bfloat16_as_ushort(__float2bfloat16_rn(-(float)(128u + zg)));
-            const uint32_t nbh = __bfloat16_as_ushort(__float2bfloat16_rn(-(float)(128u + zh)));
-            negg = nbg | (nbg << 16);
-            negh = nbh | (nbh << 16);
+            negg = dequant_bias<FORM == kQ8>(zg);
+            negh = dequant_bias<FORM == kQ8>(zh);
             if (tid < kEpi)
                 s_epi = __ldg(p.s + n0 + (tid & (kRowsPerCta - 1)));
         }
@@ -199,16 +218,16 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                     const uint32_t wgw = j ? wgv.y : wgv.x, whw = j ? whv.y : whv.x;
                     // codes k = 8j + {0..7}: nibbles (m, m + 4) hold the pair k = 2m, 2m + 1,
                     // the order of the activations in one uint4
-                    const uint32_t g0 = dequant_pair(wgw, negg), g1 = dequant_pair(wgw >> 4, negg);
-                    const uint32_t g2 = dequant_pair(wgw >> 8, negg), g3 = dequant_pair(wgw >> 12, negg);
-                    const uint32_t h0 = dequant_pair(whw, negh), h1 = dequant_pair(whw >> 4, negh);
-                    const uint32_t h2 = dequant_pair(whw >> 8, negh), h3 = dequant_pair(whw >> 12, negh);
+                    const uint32_t g0 = dequant<FORM == kQ8>(wgw, negg), g1 = dequant<FORM == kQ8>(wgw >> 4, negg);
+                    const uint32_t g2 = dequant<FORM == kQ8>(wgw >> 8, negg), g3 = dequant<FORM == kQ8>(wgw >> 12, negg);
+                    const uint32_t h0 = dequant<FORM == kQ8>(whw, negh), h1 = dequant<FORM == kQ8>(whw >> 4, negh);
+                    const uint32_t h2 = dequant<FORM == kQ8>(whw >> 8, negh), h3 = dequant<FORM == kQ8>(whw >> 12, negh);
 #pragma unroll
                     for (int n = 0; n < T; ++n) {
                         const uint4 v = xv[n][j];
                         float (&a)[4] = j ? acc2[n] : acc[n];
-                        mma_bf16_16816(a, g0, h0, g1, h1, v.x, v.y);
-                        mma_bf16_16816(a, g2, h2, g3, h3, v.z, v.w);
+                        mma_16816<FORM == kQ8>(a, g0, h0, g1, h1, v.x, v.y);
+                        mma_16816<FORM == kQ8>(a, g2, h2, g3, h3, v.z, v.w);
                     }
                 }
             } else {
@@ -235,6 +254,18 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         };
         const int sb0 = warp * nsb_cta / W, sb1 = (warp + 1) * nsb_cta / W;
         pdl_wait();
+        // epilogue operands of this thread's output, in flight during the product
+        EpiOperands eo;
+        float xs_epi = 1.f;
+        if constexpr (FORM != kPlain) {
+            const int t = tid / kRowsPerCta;
+            const int64_t n = n0 + (tid & (kRowsPerCta - 1));
+            if (!is_u && tid < kEpi && t < p.M && n < p.N) {
+                eo = epi_load(p.epi, t, n, p.N);
+                if (FORM == kQ8)
+                    xs_epi = __ldg(p.epi.xs + t);
+            }
+        }
         bool ok = true;
         if (p.xstage && !is_u) {
             // A few tokens: the row CTA's activations x[t][0 .. K) are staged in
@@ -248,7 +279,7 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             for (int c = tid; c < mrows * per_row; c += kConsumers) {
                 const int t = c / per_row, c8 = c - t * per_row;
                 const int64_t k = kbase + 8 * c8;
-                const uint4 v = k < p.K ? ld_nc(p.x + (int64_t)t * p.K + k) : make_uint4(0, 0, 0, 0);
+                const uint4 v = k < p.K ? load_x8<FORM>(p.x, (int64_t)t * p.K + k, false) : make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4 *>(xs + t * xst + 8 * c8) = v;
             }
             named_bar_sync(2, kConsumers);
@@ -282,9 +313,8 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 for (int n = 0; n < T; ++n) {
                     const int64_t t = 8 * n + gid;
                     if (t < p.M && k < p.K) {
-                        const uint16_t *src = p.x + t * p.K + k;
-                        dst[n][0] = ld_nc(src);
-                        dst[n][1] = ld_nc(src + 8);
+                        dst[n][0] = load_x8<FORM>(p.x, t * p.K + k, is_u);
+                        dst[n][1] = load_x8<FORM>(p.x, t * p.K + k + 8, is_u);
                     } else {
                         dst[n][0] = make_uint4(0, 0, 0, 0);
                         dst[n][1] = dst[n][0];
@@ -359,9 +389,15 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                                 v0.w * bf16_hi(bv.y) + v1.x * bf16_lo(bv.z) + v1.y * bf16_hi(bv.z) +
                                 v1.z * bf16_lo(bv.w) + v1.w * bf16_hi(bv.w);
                     }
-                    const float g = 1.0f / (1.0f + expf(-(u0[t] + p.b_g)));
+                    // (form kQ8: u is that of the 8-bit values, xs_epi times it the layer's)
+                    const float u_gate = FORM == kQ8 ? xs_epi * u0[t] : u0[t];
+                    const float g = 1.0f / (1.0f + expf(-(u_gate + p.b_g)));
                     out += g * corr;
                 }
+                if constexpr (FORM == kQ8)
+                    out *= xs_epi;
+                if constexpr (FORM != kPlain)
+                    out = epi_apply(p.epi, out, eo);
                 const int64_t n = n0 + row;
                 if (t < p.M && n < p.N)
                     p.y[(int64_t)t * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
@@ -443,10 +479,16 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
     __syncthreads();
 }
 
-template <int T, int W, int MINB>
-const void *rows_ptr()
+using RowsFn = void (*)(CUtensorMap, CUtensorMap, RowsParams);
+
+// The kernel for T token groups in a form.
+RowsFn rows_fn(int T, int form)
 {
-    return reinterpret_cast<const void *>(decode_rows_kernel<T, W, MINB>);
+    switch (form) {
+    case kEpi: return T == 1 ? decode_rows_kernel<1, 16, 2, kEpi> : decode_rows_kernel<2, 8, 2, kEpi>;
+    case kQ8: return T == 1 ? decode_rows_kernel<1, 16, 2, kQ8> : decode_rows_kernel<2, 8, 2, kQ8>;
+    default: return T == 1 ? decode_rows_kernel<1, 16, 2, kPlain> : decode_rows_kernel<2, 8, 2, kPlain>;
+    }
 }
 
 // Consumer warps per CTA: sixteen for one token group, eight for two.
@@ -494,7 +536,7 @@ bool decode_rows_shape(const Packed &pk)
 
 // The grid (row CTAs and, with the EC, the CTAs of u) must be one wave of two
 // CTAs per SM: a second wave would wait for a whole first one.
-bool decode_rows_fits(const Packed &pk, int64_t M, int num_sms)
+bool decode_rows_fits(const Packed &pk, int64_t M, int num_sms, int form)
 {
     const int64_t ctas = pk.Np / kRowsPerCta + (pk.r > 0 ? (int64_t)pk.R1p / kRowsPerCta * kECSplit : 0);
     if (!(M >= 1 && M <= kRowsMaxTokens && decode_rows_shape(pk) && ctas <= 2LL * num_sms))
@@ -503,7 +545,7 @@ bool decode_rows_fits(const Packed &pk, int64_t M, int num_sms)
     // CTAs wait, bounded, for the CTAs of u)
     RowsPlan pl;
     rows_plan(pk, M, pl);
-    const void *fn = pl.T == 1 ? rows_ptr<1, 16, 2>() : rows_ptr<2, 8, 2>();
+    const void *fn = reinterpret_cast<const void *>(rows_fn(pl.T, form));
     return grid_is_one_wave(fn, 32 * pl.W + 32, pl.smem, 1, ctas, num_sms);
 }
 
@@ -539,14 +581,16 @@ cudaError_t decode_rows_prepare(const Packed &pk, void **maps)
 void decode_rows_free(void *maps) { delete static_cast<RowsMaps *>(maps); }
 
 cudaError_t launch_decode_rows(const Packed &pk, const void *maps, const void *x, void *y, int64_t M, bool ec,
-                               const DecodeWork &w, int *status, cudaStream_t st, int num_sms)
+                               const DecodeWork &w, int *status, cudaStream_t st, int num_sms, int form,
+                               const Epilogue &epi)
 {
-    if (!decode_rows_fits(pk, M, num_sms) || !maps)
+    if (!decode_rows_fits(pk, M, num_sms, form) || !maps)
         return cudaErrorInvalidValue;
     const RowsMaps *m = static_cast<const RowsMaps *>(maps);
     const bool use_ec = ec && pk.r > 0;
     RowsParams p;
-    p.x = static_cast<const uint16_t *>(x);
+    p.x = x;
+    p.epi = epi;
     p.Bt = pk.Bt;
     p.s = pk.s;
     p.z = pk.z;
@@ -583,8 +627,8 @@ cudaError_t launch_decode_rows(const Packed &pk, const void *maps, const void *x
     const int T = pl.T;
     const int W = pl.W;
     const size_t smem = pl.smem;
-    const void *fn = T == 1 ? rows_ptr<1, 16, 2>() : rows_ptr<2, 8, 2>();
-    cudaError_t e = raise_smem_limit(fn, smem);
+    const RowsFn fn = rows_fn(T, form);
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
@@ -597,9 +641,7 @@ cudaError_t launch_decode_rows(const Packed &pk, const void *maps, const void *x
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (T == 1)
-        return cudaLaunchKernelEx(&cfg, decode_rows_kernel<1, 16, 2>, m->codes, m->g, p);
-    return cudaLaunchKernelEx(&cfg, decode_rows_kernel<2, 8, 2>, m->codes, m->g, p);
+    return cudaLaunchKernelEx(&cfg, fn, m->codes, m->g, p);
 }
 
 }  // namespace spear

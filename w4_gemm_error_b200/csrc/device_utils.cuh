@@ -71,6 +71,53 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with f16 operands.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// As dequant_pair, in f16: the nibble in the low mantissa bits of 1024.0
+// (0x6400) is 1024 + q, and subtracting 1024 + zp is exact.
+__device__ __forceinline__ uint32_t dequant_pair_f16(uint32_t w_shifted, uint32_t neg_bias)
+{
+    const uint32_t t = lop3_and_or(w_shifted, 0x000F000Fu, 0x64006400u);
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(t), "r"(neg_bias));
+    return d;
+}
+
+// The three of them in the type of the activations' pairs: f16 (F16) or bf16.
+template <bool F16>
+__device__ __forceinline__ uint32_t dequant_bias(uint32_t zp)
+{
+    const uint32_t b = F16 ? 0x8000u | (0x6400u + zp)   // -(1024 + zp): an f16 there counts in ones
+                           : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(-(float)(128u + zp)));
+    return b | (b << 16);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t dequant(uint32_t w_shifted, uint32_t neg_bias)
+{
+    if constexpr (F16)
+        return dequant_pair_f16(w_shifted, neg_bias);
+    else
+        return dequant_pair(w_shifted, neg_bias);
+}
+template <bool F16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    if constexpr (F16)
+        mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
+    else
+        mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
+}
+
 // Streaming 16-byte load that is read once (no L1 allocation).
 __device__ __forceinline__ uint4 ld_stream(const void *p)
 {
@@ -113,6 +160,35 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
+}
+
+// Two fp32 values as e4m3 (round to nearest even, saturating), lo in the low byte.
+__device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi)
+{
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Two e4m3 values (low byte first) as f16x2: every e4m3 value, NaN included, is one of f16.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(v));
+    return d;
+}
+
+// f16x2 as bf16x2; exact for values that came from e4m3 (four significant bits).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t v)
+{
+    float lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.f32.f16 %0, a;\n\t"
+        "cvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(v));
+    return pack_bf16x2(lo, hi);
 }
 
 }  // namespace spear

@@ -33,6 +33,8 @@ struct spear_w4ec {
     // staging for forward_host
     void *x_stage = nullptr;
     void *y_stage = nullptr;
+    // 8-bit activations with padded rows, for K that is no multiple of 16: [max_M][K + 8]
+    uint8_t *xq_pad = nullptr;
     // dispatch table: flags per M bucket, 0 = not tuned
     uint32_t table[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};
     // measured microseconds per forward, per M bucket and choice (see

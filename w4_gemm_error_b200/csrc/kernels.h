@@ -104,17 +104,24 @@ void decode_free(DecodeWork &w);
 size_t decode_u_floats(const Packed &pk);
 cudaError_t launch_decode(const Packed &pk, const void *x, void *y, int64_t M, bool ec, const DecodeWork &w,
                           int *status, cudaStream_t st, int num_sms);
+// The same in a form of epilogue.cuh (kPlain, kEpi, kQ8): rows of x are ldx
+// elements apart (ldx = K for bf16; a multiple of 16 for e4m3).
+struct Epilogue;
+cudaError_t launch_decode_form(const Packed &pk, const void *x, int64_t ldx, void *y, int64_t M, bool ec,
+                               const DecodeWork &w, int *status, cudaStream_t st, int num_sms, int form,
+                               const Epilogue &epi);
 
 // ---- decode kernel with one CTA per 16 weight rows over the whole of K (up to
 // 16 tokens, K a multiple of 64 and at most 8192, a grid of one wave of two
 // CTAs per SM); launch_decode takes it when it fits.  `maps` is filled by
 // decode_rows_prepare; it uses the DecodeWork buffers and prefetch hint.
 bool decode_rows_shape(const Packed &pk);
-bool decode_rows_fits(const Packed &pk, int64_t M, int num_sms);
+bool decode_rows_fits(const Packed &pk, int64_t M, int num_sms, int form);
 cudaError_t decode_rows_prepare(const Packed &pk, void **maps);
 void decode_rows_free(void *maps);
 cudaError_t launch_decode_rows(const Packed &pk, const void *maps, const void *x, void *y, int64_t M, bool ec,
-                               const DecodeWork &w, int *status, cudaStream_t st, int num_sms);
+                               const DecodeWork &w, int *status, cudaStream_t st, int num_sms, int form,
+                               const Epilogue &epi);
 
 // ---- decode kernel for up to 16 tokens with K split over a thread-block
 // cluster (each CTA stages only its slice of x; partial tiles summed over

@@ -13,6 +13,7 @@
 
 #include "spear_w4ec.h"
 #include "device_utils.cuh"
+#include "epilogue.cuh"
 #include "handle.h"
 #include "kernels.h"
 #include "tc_gemm.h"
@@ -66,6 +67,7 @@ void free_all(spear_w4ec *h)
     cudaFree(h->vready);
     cudaFree(h->x_stage);
     cudaFree(h->y_stage);
+    cudaFree(h->xq_pad);
 }
 
 int from_cuda(cudaError_t e)
@@ -126,16 +128,36 @@ cudaError_t run_prepass(const spear_w4ec *h, const void *x, int64_t M, bool tf32
     return launch_prepass(h->pk, x, M, h->v, tf32, h->gbuf, h->pre, st, h->num_sms, ready, ready && M <= 64);
 }
 
-int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t flags, cudaStream_t st)
+// The epilogue of tokens t0 and up.
+Epilogue epi_rows(Epilogue e, int64_t t0, int64_t N)
+{
+    if (e.mul)
+        e.mul += t0 * N;
+    if (e.residual)
+        e.residual += t0 * N;
+    if (e.xs)
+        e.xs += t0;
+    return e;
+}
+
+// form and epi: see epilogue.cuh.  The forms with an epilogue form the EC in
+// the same kernel as the product, whatever placement the table holds: y is
+// written once, after its last operand was read.
+int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t flags, cudaStream_t st,
+                int form = kPlain, const Epilogue &epi = Epilogue())
 {
     const Packed &pk = h->pk;
     const bool ec = pk.r > 0 && !(flags & SPEAR_EC_OFF);
-    const uint32_t choice = resolve(h, M, flags);
+    uint32_t choice = resolve(h, M, flags);
+    if (form != kPlain && !(flags & SPEAR_FORCE_SPLIT))
+        choice = (choice & ~(uint32_t)SPEAR_FORCE_SPLIT) | SPEAR_FORCE_FUSED;
     if ((choice & SPEAR_FORCE_DECODE) && (choice & SPEAR_FORCE_TC))
         return SPEAR_ERR_INVALID;
     if ((choice & SPEAR_FORCE_FUSED) && (choice & SPEAR_FORCE_SPLIT))
         return SPEAR_ERR_INVALID;
     const bool fused = (choice & SPEAR_FORCE_FUSED) != 0;
+    if (form != kPlain && !fused)
+        return SPEAR_ERR_UNSUPPORTED;
     if (h->fault_launch)
         return SPEAR_ERR_CUDA;
     cudaError_t e = cudaSuccess;
@@ -157,7 +179,7 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
         if (!tc_supported(h))
             return SPEAR_ERR_UNSUPPORTED;
         e = launch_tc(pk, x, y, M, h->v, ec && fused, h->tc, h->status, h->fault_timeout, st, h->num_sms,
-                      early ? h->vready : nullptr, expected);
+                      early ? h->vready : nullptr, expected, form == kEpi ? &epi : nullptr);
         if (e != cudaSuccess || (early && h->fault_timeout)) {
             // nothing will reset the prepass's counts: clear them for the next forward
             cudaMemsetAsync(h->vready, 0, 2 * sizeof(unsigned), st);
@@ -167,9 +189,9 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
     } else {
         for (int64_t t0 = 0; t0 < M; t0 += kDecodeMaxTokens) {
             const int64_t m = std::min<int64_t>(kDecodeMaxTokens, M - t0);
-            e = launch_decode(pk, static_cast<const uint16_t *>(x) + t0 * pk.K,
-                              static_cast<uint16_t *>(y) + t0 * pk.N, m, ec && fused, h->dec, h->status, st,
-                              h->num_sms);
+            e = launch_decode_form(pk, static_cast<const uint16_t *>(x) + t0 * pk.K, pk.K,
+                                   static_cast<uint16_t *>(y) + t0 * pk.N, m, ec && fused, h->dec, h->status, st,
+                                   h->num_sms, form, epi_rows(epi, t0, pk.N));
             if (e != cudaSuccess)
                 return from_cuda(e);
         }
@@ -179,6 +201,98 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
         if (e != cudaSuccess)
             return from_cuda(e);
     }
+    return SPEAR_OK;
+}
+
+// Rows of 8-bit activations whose length is no multiple of 16 (it is one of 8)
+// with the row pitch that the TMA copies need.
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint2 *src, uint2 *dst, int64_t M, int units)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t n = M * (units + 1);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / (units + 1);
+        const int u = (int)(i - t * (units + 1));
+        dst[i] = u < units ? src[t * units + u] : make_uint2(0u, 0u);
+    }
+}
+
+// The forward pass on e4m3 activations.
+int run_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y, int64_t M, uint32_t flags,
+                   cudaStream_t st, Epilogue epi)
+{
+    const Packed &pk = h->pk;
+    const bool ec = pk.r > 0 && !(flags & SPEAR_EC_OFF);
+    if ((flags & SPEAR_FORCE_DECODE) && (flags & SPEAR_FORCE_TC))
+        return SPEAR_ERR_INVALID;
+    if ((flags & SPEAR_FORCE_FUSED) && (flags & SPEAR_FORCE_SPLIT))
+        return SPEAR_ERR_INVALID;
+    if (flags & (SPEAR_FORCE_SPLIT | SPEAR_FORCE_TC))
+        return SPEAR_ERR_UNSUPPORTED;
+    if (!decode_supported(pk, h->num_sms))
+        return SPEAR_ERR_UNSUPPORTED;
+    if (h->fault_launch)
+        return SPEAR_ERR_CUDA;
+    epi.xs = xs;
+    int64_t ldx = pk.K;
+    if (ldx % 16) {
+        const int units = (int)(pk.K / 8);
+        const int64_t blocks = std::min<int64_t>((M * (units + 1) + 255) / 256, 8 * h->num_sms);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, pad_rows_kernel, static_cast<const uint2 *>(xq),
+                                                 reinterpret_cast<uint2 *>(h->xq_pad), M, units);
+        if (e != cudaSuccess)
+            return from_cuda(e);
+        xq = h->xq_pad;
+        ldx = pk.K + 8;
+    }
+    for (int64_t t0 = 0; t0 < M; t0 += kDecodeMaxTokens) {
+        const int64_t m = std::min<int64_t>(kDecodeMaxTokens, M - t0);
+        const cudaError_t e = launch_decode_form(pk, static_cast<const uint8_t *>(xq) + t0 * ldx, ldx,
+                                                 static_cast<uint16_t *>(y) + t0 * pk.N, m, ec, h->dec, h->status,
+                                                 st, h->num_sms, kQ8, epi_rows(epi, t0, pk.N));
+        if (e != cudaSuccess)
+            return from_cuda(e);
+    }
+    return SPEAR_OK;
+}
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+// Check a caller's epilogue and take it over.  mul and residual may be y
+// itself (each output's operands are read by the thread that writes it, before
+// it does); any other overlap with y is refused.
+int take_epilogue(const spear_w4ec *h, const spear_w4ec_epilogue *ep, const void *y, int64_t M, Epilogue *out)
+{
+    *out = Epilogue();
+    if (!ep)
+        return SPEAR_OK;
+    if (ep->act < SPEAR_ACT_NONE || ep->act > SPEAR_ACT_GELU_TANH || ep->reserved != 0)
+        return SPEAR_ERR_INVALID;
+    if (!aligned16(ep->bias) || !aligned16(ep->mul) || !aligned16(ep->residual))
+        return SPEAR_ERR_INVALID;
+    const size_t ny = (size_t)M * (size_t)h->pk.N * 2;
+    if (overlap(ep->bias, (size_t)h->pk.N * 2, y, ny) || (ep->mul != y && overlap(ep->mul, ny, y, ny)) ||
+        (ep->residual != y && overlap(ep->residual, ny, y, ny)))
+        return SPEAR_ERR_INVALID;
+    out->bias = static_cast<const uint16_t *>(ep->bias);
+    out->mul = static_cast<const uint16_t *>(ep->mul);
+    out->residual = static_cast<const uint16_t *>(ep->residual);
+    out->act = ep->act;
     return SPEAR_OK;
 }
 
@@ -326,6 +440,8 @@ int spear_w4ec_create(spear_w4ec **out, int64_t K, int64_t N, int32_t r, const s
     chk(tc_alloc(pk, h->max_M, h->num_sms, h->tc));
     chk(alloc_zero(&h->status, 1));
     chk(alloc_zero(&h->vready, 2));
+    if (K % 16)
+        chk(alloc_zero(&h->xq_pad, (size_t)h->max_M * (size_t)(K + 8)));
     if (e == cudaSuccess)
         e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
@@ -371,6 +487,52 @@ int spear_w4ec_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, u
     if (!guard.ok())
         return SPEAR_ERR_CUDA;
     return run_forward(h, x, y, M, flags, static_cast<cudaStream_t>(stream));
+}
+
+int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M, const spear_w4ec_epilogue *ep,
+                          uint32_t flags, void *stream)
+{
+    if (!h || M < 0)
+        return SPEAR_ERR_INVALID;
+    if (M == 0)
+        return SPEAR_OK;
+    if (!h->packed)
+        return SPEAR_ERR_STATE;
+    if (M > h->max_M || !x || !y || !aligned16(x) || !aligned16(y) ||
+        overlap(x, (size_t)M * (size_t)h->pk.K * 2, y, (size_t)M * (size_t)h->pk.N * 2))
+        return SPEAR_ERR_INVALID;
+    Epilogue epi;
+    const int rc = take_epilogue(h, ep, y, M, &epi);
+    if (rc != SPEAR_OK)
+        return rc;
+    DeviceGuard guard(h->device);
+    if (!guard.ok())
+        return SPEAR_ERR_CUDA;
+    return run_forward(h, x, y, M, flags, static_cast<cudaStream_t>(stream), kEpi, epi);
+}
+
+int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y, int64_t M,
+                          const spear_w4ec_epilogue *ep, uint32_t flags, void *stream)
+{
+    if (!h || M < 0)
+        return SPEAR_ERR_INVALID;
+    if (M == 0)
+        return SPEAR_OK;
+    if (!h->packed)
+        return SPEAR_ERR_STATE;
+    const size_t ny = (size_t)M * (size_t)h->pk.N * 2;
+    if (M > h->max_M || !xq || !xs || !y || !aligned16(xq) || !aligned16(y) ||
+        (reinterpret_cast<uintptr_t>(xs) & 3u) != 0 || overlap(xq, (size_t)M * (size_t)h->pk.K, y, ny) ||
+        overlap(xs, (size_t)M * 4, y, ny))
+        return SPEAR_ERR_INVALID;
+    Epilogue epi;
+    const int rc = take_epilogue(h, ep, y, M, &epi);
+    if (rc != SPEAR_OK)
+        return rc;
+    DeviceGuard guard(h->device);
+    if (!guard.ok())
+        return SPEAR_ERR_CUDA;
+    return run_forward_q8(h, xq, xs, y, M, flags, static_cast<cudaStream_t>(stream), epi);
 }
 
 int spear_w4ec_forward_host(spear_w4ec *h, const void *x_host, void *y_host, int64_t M, uint32_t flags,

@@ -42,6 +42,7 @@
 #include <new>
 
 #include "async_utils.cuh"
+#include "epilogue.cuh"
 #include "tc_gemm.h"
 #include "tensor_map.h"
 
@@ -86,6 +87,7 @@ struct TcParams {
     // kernel waits for its predecessor first, as usual.
     unsigned *v_ready;
     unsigned v_expected;
+    Epilogue epi;          // form kEpi
 };
 
 struct Maps {
@@ -253,7 +255,37 @@ tc_prepass_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 
 // ---------------------------------------------------------------- the kernel
 
-template <int BN>
+// Eight outputs of channel n, tokens t .. t + 7 below M: y = e_n * acc, through
+// the epilogue in form kEpi (its eight operand loads are issued before any is
+// used; they come after the accumulator is complete, and so after every kernel
+// that this one waits for).
+template <int FORM>
+__device__ __forceinline__ void store_outputs8(const TcParams &p, int64_t t, int64_t n, float e_n, float bias,
+                                               const float (&acc)[8])
+{
+    EpiOperands eo[FORM == kEpi ? 8 : 1];
+    if constexpr (FORM == kEpi) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            eo[j].bias = bias;
+            if (p.epi.mul && t + j < p.M)
+                eo[j].mul = bf16_lo(p.epi.mul[(t + j) * p.N + n]);
+            if (p.epi.residual && t + j < p.M)
+                eo[j].residual = bf16_lo(p.epi.residual[(t + j) * p.N + n]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (t + j >= p.M)
+            continue;
+        float v = e_n * acc[j];
+        if constexpr (FORM == kEpi)
+            v = epi_apply(p.epi, v, eo[j]);
+        p.y[(t + j) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
+}
+
+template <int BN, int FORM>
 __global__ void __launch_bounds__(THREADS, 1)
 tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_codes,
                const __grid_constant__ CUtensorMap tm_bt, const __grid_constant__ CUtensorMap tm_v, TcParams p)
@@ -500,6 +532,7 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const int64_t n = (int64_t)(tile / p.n_ttiles) * BM + row;
             const float sn = p.s[n];
             const float e_n = sn != 0.0f ? sn : 1.0f;   // the EC operand was divided by it
+            const float bias = FORM == kEpi && p.epi.bias && n < p.N ? bf16_lo(__ldg(p.epi.bias + n)) : 0.f;
             if (p.ksplit == 1) {
 #pragma unroll 1
                 for (int c = 0; c < BN / 32; ++c) {
@@ -507,11 +540,12 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(32 * q) << 16) + buf * BN + 32 * c, r);
                     if (n < p.N) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int64_t t = t0 + 32 * c + j;
-                            if (t < p.M)
-                                p.y[t * p.N + n] =
-                                    __bfloat16_as_ushort(__float2bfloat16_rn(e_n * __uint_as_float(r[j])));
+                        for (int j0 = 0; j0 < 32; j0 += 8) {
+                            float a[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                a[j] = __uint_as_float(r[j0 + j]);
+                            store_outputs8<FORM>(p, t0 + 32 * c + j0, n, e_n, bias, a);
                         }
                     }
                 }
@@ -558,10 +592,8 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         for (int jj = 0; jj < 8; ++jj)
                             v[jj] += w[jj];
                     }
-#pragma unroll
-                    for (int jj = 0; jj < 8; ++jj)
-                        if (j0 + jj < jn && n < p.N)
-                            p.y[(t0 + j0 + jj) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(e_n * v[jj]));
+                    if (n < p.N)
+                        store_outputs8<FORM>(p, t0 + j0, n, e_n, bias, v);
                 }
                 if (q == 0 && lane == 0)
                     p.counters[tile] = 0u;   // for the next forward
@@ -651,9 +683,25 @@ cudaError_t tc_prepare(const Packed &pk, TcWork &w)
     return e;
 }
 
+namespace {
+
+using TcFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, TcParams);
+template <int FORM>
+TcFn tc_fn(int BN)
+{
+    switch (BN) {
+    case 32: return tc_w4ec_kernel<32, FORM>;
+    case 64: return tc_w4ec_kernel<64, FORM>;
+    case 128: return tc_w4ec_kernel<128, FORM>;
+    default: return tc_w4ec_kernel<256, FORM>;
+    }
+}
+
+}  // namespace
+
 cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                       const TcWork &w, int *status, bool zero_wait_budget, cudaStream_t st, int num_sms,
-                      unsigned *v_ready, unsigned v_expected)
+                      unsigned *v_ready, unsigned v_expected, const Epilogue *epi)
 {
     if (M <= 0)
         return cudaSuccess;
@@ -707,12 +755,11 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
     p.v_ready = use_ec ? v_ready : nullptr;
     p.v_expected = v_expected;
 
-    const void *fn = BN == 32 ? reinterpret_cast<const void *>(tc_w4ec_kernel<32>)
-                   : BN == 64 ? reinterpret_cast<const void *>(tc_w4ec_kernel<64>)
-                   : BN == 128 ? reinterpret_cast<const void *>(tc_w4ec_kernel<128>)
-                               : reinterpret_cast<const void *>(tc_w4ec_kernel<256>);
+    if (epi)
+        p.epi = *epi;
+    const TcFn fn = epi ? tc_fn<kEpi>(BN) : tc_fn<kPlain>(BN);
     const int smem = tc_smem_bytes(BN);
-    e = raise_smem_limit(fn, smem);
+    e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
@@ -726,12 +773,7 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const CUtensorMap &bt = use_ec ? m->bt : m->codes;
-    switch (BN) {
-    case 32: return cudaLaunchKernelEx(&cfg, tc_w4ec_kernel<32>, tm_x, m->codes, bt, tm_v, p);
-    case 64: return cudaLaunchKernelEx(&cfg, tc_w4ec_kernel<64>, tm_x, m->codes, bt, tm_v, p);
-    case 128: return cudaLaunchKernelEx(&cfg, tc_w4ec_kernel<128>, tm_x, m->codes, bt, tm_v, p);
-    default: return cudaLaunchKernelEx(&cfg, tc_w4ec_kernel<256>, tm_x, m->codes, bt, tm_v, p);
-    }
+    return cudaLaunchKernelEx(&cfg, fn, tm_x, m->codes, bt, tm_v, p);
 }
 
 }  // namespace spear

@@ -30,8 +30,9 @@ cudaError_t launch_tc_prepass(const Packed &pk, const void *x, int64_t M, float 
 // without waiting for its predecessor, which must be a prepass that counts
 // v_expected completions into v_ready[0] and starts its dependents only once x is
 // complete; v_ready[0..1] are zero between calls.
+// epi (may be null): bias, activation, multiplier and residual of the outputs.
 cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                       const TcWork &w, int *status, bool zero_wait_budget, cudaStream_t st, int num_sms,
-                      unsigned *v_ready, unsigned v_expected);
+                      unsigned *v_ready, unsigned v_expected, const Epilogue *epi = nullptr);
 
 }  // namespace spear

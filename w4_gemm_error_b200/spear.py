@@ -31,11 +31,20 @@ SPEAR_FORCE_DECODE = 8
 SPEAR_FORCE_TC = 16
 SPEAR_STACK_PERSISTENT = 32   # stack forward only: one persistent kernel for the whole stack
 
+SPEAR_ACT_NONE = 0
+SPEAR_ACT_RELU = 1
+SPEAR_ACT_SILU = 2
+SPEAR_ACT_GELU = 3
+SPEAR_ACT_GELU_TANH = 4
+ACTIVATIONS = {"none": SPEAR_ACT_NONE, "relu": SPEAR_ACT_RELU, "silu": SPEAR_ACT_SILU, "gelu": SPEAR_ACT_GELU,
+               "gelu_tanh": SPEAR_ACT_GELU_TANH}
+
 SPEAR_TP_MAX_WORLD = 8
 SPEAR_TP_IPC_HANDLE_BYTES = 64
 
 EXPORTED = ("spear_w4ec_create", "spear_w4ec_pack", "spear_w4ec_pack_asym", "spear_w4ec_import",
-            "spear_w4ec_forward", "spear_w4ec_forward_host",
+            "spear_w4ec_forward", "spear_w4ec_forward_ep", "spear_w4ec_forward_q8", "spear_w4ec_rmsnorm",
+            "spear_w4ec_quantize_q8", "spear_w4ec_forward_host",
             "spear_w4ec_destroy", "spear_w4ec_get_packed", "spear_w4ec_get_gate", "spear_w4ec_sync_status",
             "spear_w4ec_tune", "spear_w4ec_dispatch", "spear_w4ec_gate_noalloc", "spear_w4ec_set_next",
             "spear_w4ec_stack_create", "spear_w4ec_stack_forward", "spear_w4ec_stack_forward_host",
@@ -53,6 +62,12 @@ class SpearError(RuntimeError):
 
 class _Opts(ctypes.Structure):
     _fields_ = [("max_M", ctypes.c_int64), ("device", ctypes.c_int32)]
+
+
+class Epilogue(ctypes.Structure):
+    """spear_w4ec_epilogue: y = act(Y + bias) * mul + residual (0 leaves a term out)."""
+    _fields_ = [("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class StackOp(ctypes.Structure):
@@ -73,6 +88,10 @@ def _load():
         "spear_w4ec_pack_asym": [P, P, P, P, P, f32, P],
         "spear_w4ec_import": [P, P, P, P, P, P, P, f32, P],
         "spear_w4ec_forward": [P, P, P, i64, u32, P],
+        "spear_w4ec_forward_ep": [P, P, P, i64, ctypes.POINTER(Epilogue), u32, P],
+        "spear_w4ec_forward_q8": [P, P, P, P, i64, ctypes.POINTER(Epilogue), u32, P],
+        "spear_w4ec_rmsnorm": [P, P, P, f32, i64, i64, P, P, P, P, P],
+        "spear_w4ec_quantize_q8": [P, i64, i64, P, P, P],
         "spear_w4ec_forward_host": [P, P, P, i64, u32, P],
         "spear_w4ec_destroy": [P],
         "spear_w4ec_get_packed": [P, P, P, P, P],
@@ -169,6 +188,28 @@ def spear_w4ec_import(h: int, codes, s, z, A, B, w_g, b_g: float, stream=None):
 
 def spear_w4ec_forward(h: int, x, y, M: int, flags: int = 0, stream=None):
     _check(_lib.spear_w4ec_forward(h, _ptr(x), _ptr(y), M, flags, _stream(stream)), "spear_w4ec_forward")
+
+
+def spear_w4ec_forward_ep(h: int, x, y, M: int, ep=None, flags: int = 0, stream=None):
+    """ep: an Epilogue, or None."""
+    _check(_lib.spear_w4ec_forward_ep(h, _ptr(x), _ptr(y), M, None if ep is None else ctypes.byref(ep), flags,
+                                      _stream(stream)), "spear_w4ec_forward_ep")
+
+
+def spear_w4ec_forward_q8(h: int, xq, xs, y, M: int, ep=None, flags: int = 0, stream=None):
+    """ep: an Epilogue, or None."""
+    _check(_lib.spear_w4ec_forward_q8(h, _ptr(xq), _ptr(xs), _ptr(y), M, None if ep is None else ctypes.byref(ep),
+                                      flags, _stream(stream)), "spear_w4ec_forward_q8")
+
+
+def spear_w4ec_rmsnorm(x, residual, weight, eps: float, M: int, K: int, sum=None, y=None, q=None, s=None,
+                       stream=None):
+    _check(_lib.spear_w4ec_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), eps, M, K, _ptr(sum), _ptr(y), _ptr(q),
+                                   _ptr(s), _stream(stream)), "spear_w4ec_rmsnorm")
+
+
+def spear_w4ec_quantize_q8(x, M: int, K: int, q, s, stream=None):
+    _check(_lib.spear_w4ec_quantize_q8(_ptr(x), M, K, _ptr(q), _ptr(s), _stream(stream)), "spear_w4ec_quantize_q8")
 
 
 def spear_w4ec_forward_host(h: int, x_host, y_host, M: int, flags: int = 0, stream=None):
@@ -309,6 +350,93 @@ def spear_w4ec_tp_destroy(t: int):
     _check(_lib.spear_w4ec_tp_destroy(t), "spear_w4ec_tp_destroy")
 
 
+def _dev(t: torch.Tensor, dtype, shape, name, device):
+    """t's address, after checking its type, shape, layout and device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _cuda_rows(x, name):
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2):
+        raise ValueError(f"{name} must be a CUDA tensor [M, K]")
+    return x.shape[0], x.shape[1], x.device
+
+
+def _stream_on(stream, device) -> int:
+    """The given stream's handle, or that of the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+class _on:
+    """Makes a tensor's device current for a call that runs on the current one."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.device.index:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.prev != self.device.index:
+            torch.cuda.set_device(self.prev)
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None, *,
+            bf16: bool = True, q8: bool = False, out: torch.Tensor | None = None, out_q: torch.Tensor | None = None,
+            out_s: torch.Tensor | None = None, out_sum: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of x [M, K] (bf16) with the residual's addition:
+    (y, q, s, h), None for what was not asked for.
+
+    y is the norm in bf16 (``bf16``); q, s are the norm in float8_e4m3fn with
+    one float32 scale a row (``q8``), as W4ECLinear.forward_q8 takes them;
+    h = bf16(x + residual), of which the norm is taken, with a residual.  The
+    ``out*`` tensors are written where given (h may be x or residual itself),
+    else new ones."""
+    M, K, dev = _cuda_rows(x, "x")
+    if not (bf16 or q8):
+        raise ValueError("at least one of bf16 and q8 must be asked for")
+    if (out is not None and not bf16) or (not q8 and (out_q is not None or out_s is not None)) or \
+            (residual is None and out_sum is not None):
+        raise ValueError("an output tensor was given for an output that was not asked for")
+    px, pw = _dev(x, torch.bfloat16, (M, K), "x", dev), _dev(weight, torch.bfloat16, (K,), "weight", dev)
+    y = q = s = h = py = pq = ps = ph = pr = None
+    if residual is not None:
+        pr = _dev(residual, torch.bfloat16, (M, K), "residual", dev)
+        h = torch.empty_like(x) if out_sum is None else out_sum
+        ph = _dev(h, torch.bfloat16, (M, K), "out_sum", dev)
+    if bf16:
+        y = torch.empty_like(x) if out is None else out
+        py = _dev(y, torch.bfloat16, (M, K), "out", dev)
+    if q8:
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if out_q is None else out_q
+        s = torch.empty(M, dtype=torch.float32, device=dev) if out_s is None else out_s
+        pq, ps = _dev(q, torch.float8_e4m3fn, (M, K), "out_q", dev), _dev(s, torch.float32, (M,), "out_s", dev)
+    with _on(dev):
+        _check(_lib.spear_w4ec_rmsnorm(px, pr, pw, eps, M, K, ph, py, pq, ps, _stream_on(stream, dev)),
+               "spear_w4ec_rmsnorm")
+    return y, q, s, h
+
+
+def quantize_q8(x: torch.Tensor, *, out_q: torch.Tensor | None = None, out_s: torch.Tensor | None = None,
+                stream=None):
+    """x [M, K] (bf16) in 8 bits: (q float8_e4m3fn [M, K], s float32 [M]) with
+    x ~ q * s[:, None], as W4ECLinear.forward_q8 takes them."""
+    M, K, dev = _cuda_rows(x, "x")
+    px = _dev(x, torch.bfloat16, (M, K), "x", dev)
+    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if out_q is None else out_q
+    s = torch.empty(M, dtype=torch.float32, device=dev) if out_s is None else out_s
+    pq, ps = _dev(q, torch.float8_e4m3fn, (M, K), "out_q", dev), _dev(s, torch.float32, (M,), "out_s", dev)
+    with _on(dev):
+        _check(_lib.spear_w4ec_quantize_q8(px, M, K, pq, ps, _stream_on(stream, dev)), "spear_w4ec_quantize_q8")
+    return q, s
+
+
 class W4ECLinear:
     """Owning wrapper of one packed layer (create + pack; destroy on close).
 
@@ -364,6 +492,45 @@ class W4ECLinear:
         return y
 
     __call__ = forward
+
+    def _epilogue(self, M, act, bias, mul, residual, dev):
+        try:
+            code = ACTIVATIONS[act]
+        except (KeyError, TypeError):
+            raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}") from None
+        return Epilogue(None if bias is None else _dev(bias, torch.bfloat16, (self.N,), "bias", dev),
+                        None if mul is None else _dev(mul, torch.bfloat16, (M, self.N), "mul", dev),
+                        None if residual is None else _dev(residual, torch.bfloat16, (M, self.N), "residual", dev),
+                        code, 0)
+
+    def forward_ep(self, x: torch.Tensor, *, act: str = "none", bias: torch.Tensor | None = None,
+                   mul: torch.Tensor | None = None, residual: torch.Tensor | None = None, flags: int = 0,
+                   out: torch.Tensor | None = None, stream=None):
+        """act(forward(x) + bias) * mul + residual in one pass, rounded once.
+        act: "none", "relu", "silu", "gelu" or "gelu_tanh"; bias bf16 [N]; mul
+        and residual bf16 [M, N] (each may be ``out`` itself)."""
+        M, _, dev = _cuda_rows(x, "x")
+        px = _dev(x, torch.bfloat16, (M, self.K), "x", dev)
+        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=dev) if out is None else out
+        py = _dev(y, torch.bfloat16, (M, self.N), "out", dev)
+        ep = self._epilogue(M, act, bias, mul, residual, dev)
+        _check(_lib.spear_w4ec_forward_ep(self.h, px, py, M, ctypes.byref(ep), flags, _stream_on(stream, dev)),
+               "spear_w4ec_forward_ep")
+        return y
+
+    def forward_q8(self, xq: torch.Tensor, xs: torch.Tensor, *, act: str = "none", bias: torch.Tensor | None = None,
+                   mul: torch.Tensor | None = None, residual: torch.Tensor | None = None, flags: int = 0,
+                   out: torch.Tensor | None = None, stream=None):
+        """forward_ep on 8-bit activations x = xq * xs[:, None] (float8_e4m3fn
+        [M, K] and float32 [M], as rmsnorm and quantize_q8 make them)."""
+        M, _, dev = _cuda_rows(xq, "xq")
+        px, ps = _dev(xq, torch.float8_e4m3fn, (M, self.K), "xq", dev), _dev(xs, torch.float32, (M,), "xs", dev)
+        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=dev) if out is None else out
+        py = _dev(y, torch.bfloat16, (M, self.N), "out", dev)
+        ep = self._epilogue(M, act, bias, mul, residual, dev)
+        _check(_lib.spear_w4ec_forward_q8(self.h, px, ps, py, M, ctypes.byref(ep), flags, _stream_on(stream, dev)),
+               "spear_w4ec_forward_q8")
+        return y
 
     def packed(self, stream=None):
         codes = torch.empty((self.N, self.K // 8), dtype=torch.int32, device=self.device)
