@@ -62,6 +62,20 @@ def test_against_float64(kind, M, K, N, r):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("path", ["decode", "tcgen05"])
+@pytest.mark.parametrize("M", [1, 8, 33, 60, 100, 260])
+@pytest.mark.parametrize("K,N,r", [(1032, 520, 40), (4096, 256, 32), (520, 136, 0)])
+def test_either_kernel_family_at_any_size(kind, path, M, K, N, r):
+    from w4_gemm_error_b200.spear import SPEAR_FORCE_DECODE, SPEAR_FORCE_TC
+    lay = LayerRef(K, N, r, seed=M)
+    lin = lay.make(M)
+    ep = dict(act="silu", **operands(lay, M, True, False, True))
+    y, x = run(lin, lay, M, kind, flags=SPEAR_FORCE_DECODE if path == "decode" else SPEAR_FORCE_TC, **ep)
+    assert_layer(y, lay, x, (kind, path), **ep)
+    assert lin.status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
 @pytest.mark.parametrize("M", [1, 5, 24, 70, 300])
 def test_every_term_and_the_ec_off(kind, M):
     from w4_gemm_error_b200.spear import SPEAR_EC_OFF

@@ -59,6 +59,18 @@ __device__ __forceinline__ uint32_t dequant_pair_mul(uint32_t w_shifted, uint32_
     return fma_bf16x2(t, mul, neg_bias);
 }
 
+// The eight codes of a stored word as e4m3, k = 8j + {0..3} in lo and + {4..7}
+// in hi (one code a byte).  No arithmetic is needed: e4m3 counts linearly from
+// zero in steps of 2^-9 up to 2^-5 (its subnormals and its first binade have
+// the same spacing), so the byte 0x0q IS the value 2^-9 q.  nib = 0x0F0F0F0F,
+// or 0 for a row whose weights are all 0.
+__device__ __forceinline__ void nibbles_to_e4m3(uint32_t w, uint32_t nib, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t a = w & nib, b = (w >> 4) & nib;   // bytes: codes 0, 4, 1, 5 and 2, 6, 3, 7
+    lo = prmt(a, b, 0x6420);
+    hi = prmt(a, b, 0x7531);
+}
+
 // D (16x8 fp32) += A (16x16 bf16, row) * B (16x8 bf16, col).  Not volatile: its
 // only effect is on d, so the compiler may interleave independent MMAs.
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,

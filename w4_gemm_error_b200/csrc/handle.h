@@ -28,6 +28,7 @@ struct spear_w4ec {
     PrepassWork pre{};
     DecodeWork dec{};
     TcWork tc{};
+    spear::PrepassQ8Work preq8{};
     int *status = nullptr;      // sticky device status bits
     unsigned *vready = nullptr; // prepass -> tcgen05 kernel: [0] counts of v written, [1] CTAs done
     // staging for forward_host

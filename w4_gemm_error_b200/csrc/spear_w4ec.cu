@@ -68,6 +68,7 @@ void free_all(spear_w4ec *h)
     cudaFree(h->x_stage);
     cudaFree(h->y_stage);
     cudaFree(h->xq_pad);
+    prepass_q8_free(h->preq8);
 }
 
 int from_cuda(cudaError_t e)
@@ -80,6 +81,7 @@ int from_cuda(cudaError_t e)
 }
 
 bool tc_supported(const spear_w4ec *h) { return tc_available(h->pk); }
+
 
 // Kernel family and EC placement for M tokens: an explicit request, the tuned
 // table entry, or the default (the split-K decode kernel for a few tokens,
@@ -179,7 +181,7 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
         if (!tc_supported(h))
             return SPEAR_ERR_UNSUPPORTED;
         e = launch_tc(pk, x, y, M, h->v, ec && fused, h->tc, h->status, h->fault_timeout, st, h->num_sms,
-                      early ? h->vready : nullptr, expected, form == kEpi ? &epi : nullptr);
+                      early ? h->vready : nullptr, expected, form, epi, pk.K, nullptr);
         if (e != cudaSuccess || (early && h->fault_timeout)) {
             // nothing will reset the prepass's counts: clear them for the next forward
             cudaMemsetAsync(h->vready, 0, 2 * sizeof(unsigned), st);
@@ -228,9 +230,12 @@ int run_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y
         return SPEAR_ERR_INVALID;
     if ((flags & SPEAR_FORCE_FUSED) && (flags & SPEAR_FORCE_SPLIT))
         return SPEAR_ERR_INVALID;
-    if (flags & (SPEAR_FORCE_SPLIT | SPEAR_FORCE_TC))
+    if (flags & SPEAR_FORCE_SPLIT)
         return SPEAR_ERR_UNSUPPORTED;
-    if (!decode_supported(pk, h->num_sms))
+    uint32_t path = flags & (SPEAR_FORCE_DECODE | SPEAR_FORCE_TC);
+    if (!path)
+        path = default_path(h, M);
+    if (!path_supported(h, path))
         return SPEAR_ERR_UNSUPPORTED;
     if (h->fault_launch)
         return SPEAR_ERR_CUDA;
@@ -254,6 +259,20 @@ int run_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y
             return from_cuda(e);
         xq = h->xq_pad;
         ldx = pk.K + 8;
+    }
+    if (path == SPEAR_FORCE_TC) {
+        // as in run_forward: with the EC the product's main stages start beside
+        // the prepass, which counts what it has written into vready
+        unsigned expected = 0;
+        cudaError_t e = launch_prepass_q8(pk, xq, ldx, xs, M, ec, h->v, h->preq8, st, h->num_sms,
+                                          ec ? h->vready : nullptr, &expected);
+        if (e != cudaSuccess)
+            return from_cuda(e);
+        e = launch_tc(pk, xq, y, M, h->v, ec, h->tc, h->status, h->fault_timeout, st, h->num_sms,
+                      ec ? h->vready : nullptr, expected, kQ8, epi, ldx, h->preq8.rowc);
+        if (e != cudaSuccess || (ec && h->fault_timeout))
+            cudaMemsetAsync(h->vready, 0, 2 * sizeof(unsigned), st);
+        return from_cuda(e);
     }
     for (int64_t t0 = 0; t0 < M; t0 += kDecodeMaxTokens) {
         const int64_t m = std::min<int64_t>(kDecodeMaxTokens, M - t0);
@@ -440,6 +459,7 @@ int spear_w4ec_create(spear_w4ec **out, int64_t K, int64_t N, int32_t r, const s
     chk(tc_alloc(pk, h->max_M, h->num_sms, h->tc));
     chk(alloc_zero(&h->status, 1));
     chk(alloc_zero(&h->vready, 2));
+    chk(prepass_q8_alloc(pk, h->max_M, h->num_sms, h->preq8));
     if (K % 16)
         chk(alloc_zero(&h->xq_pad, (size_t)h->max_M * (size_t)(K + 8)));
     if (e == cudaSuccess)

@@ -50,19 +50,30 @@ namespace spear {
 namespace {
 
 constexpr int BM = 128;                       // weight rows per tile (TMEM lanes)
-constexpr int BK = 64;                        // k per stage: one 128-byte swizzle atom of bf16
-constexpr int A_BYTES = BM * BK * 2;          // 16 KB dequantised weights (or B^T on EC stages)
-constexpr int C_BYTES = BM * BK / 2;          // 4 KB int4 codes
+constexpr int ROW_BYTES = 128;                // one swizzle atom: a stage's k of one row of either operand
+// k per stage: 64 bf16 or (form kQ8) 128 e4m3 values
+__host__ __device__ constexpr int tc_bk(int form) { return form == kQ8 ? 128 : 64; }
+constexpr int A_BYTES = BM * ROW_BYTES;       // 16 KB dequantised weights (or B^T on EC stages)
+__host__ __device__ constexpr int tc_c_bytes(int form) { return BM * tc_bk(form) / 2; }   // int4 codes
 constexpr int THREADS = 704;   // 22 warps: TMA, MMA, 2 x 8 dequantisers, 4 epilogue
 
 // Token tile BN (the MMA N: 32, 64, 128 or 256) and what depends on it: the
-// activation tile of a stage (BN x 64 bf16, or v on EC stages), the ring depth
-// (more stages for narrower tiles, within about 210 KB) and two accumulators of
+// activation tile of a stage (BN rows, or v on EC stages), the ring depth
+// (more stages for narrower tiles, within about 225 KB) and two accumulators of
 // BN columns in TMEM.
-__host__ __device__ constexpr int tc_b_bytes(int BN) { return BN * BK * 2; }
-__host__ __device__ constexpr int tc_stage_bytes(int BN) { return A_BYTES + tc_b_bytes(BN) + C_BYTES; }
-__host__ __device__ constexpr int tc_stages(int BN) { return BN >= 256 ? 4 : (BN >= 128 ? 6 : (BN >= 64 ? 7 : 8)); }
-__host__ __device__ constexpr int tc_smem_bytes(int BN) { return tc_stages(BN) * tc_stage_bytes(BN) + 1024; }
+__host__ __device__ constexpr int tc_b_bytes(int BN) { return BN * ROW_BYTES; }
+__host__ __device__ constexpr int tc_stage_bytes(int BN, int form)
+{
+    return A_BYTES + tc_b_bytes(BN) + tc_c_bytes(form);
+}
+__host__ __device__ constexpr int tc_stages(int BN, int form)
+{
+    return BN >= 256 ? 4 : (BN >= 128 ? (form == kQ8 ? 5 : 6) : (BN >= 64 ? 7 : 8));
+}
+__host__ __device__ constexpr int tc_smem_bytes(int BN, int form)
+{
+    return tc_stages(BN, form) * tc_stage_bytes(BN, form) + 1024;
+}
 
 struct TcParams {
     int64_t M, N;
@@ -87,11 +98,13 @@ struct TcParams {
     // kernel waits for its predecessor first, as usual.
     unsigned *v_ready;
     unsigned v_expected;
-    Epilogue epi;          // form kEpi
+    Epilogue epi;          // forms kEpi and kQ8
+    const float2 *rowc;    // form kQ8: [M] (2^9 xs[t], 2^-9 sum_k xq[t,k]) from the prepass
 };
 
 struct Maps {
     CUtensorMap codes;
+    CUtensorMap codes128;   // the same codes in boxes of 128 k x 64 rows, 64B swizzle (form kQ8)
     CUtensorMap bt;
     CUtensorMap g;   // G = [w_g; A^T] [R1p][Kp] bf16, boxes of 64 x R1p, 128B swizzle
 };
@@ -259,12 +272,19 @@ tc_prepass_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 // the epilogue in form kEpi (its eight operand loads are issued before any is
 // used; they come after the accumulator is complete, and so after every kernel
 // that this one waits for).
+// Form kQ8: acc is 2^-9 sum_k xq q (the codes q themselves are the e4m3 bit
+// patterns of 2^-9 q), so that Y = xs e_n (2^9 acc - z sum_k xq).
 template <int FORM>
-__device__ __forceinline__ void store_outputs8(const TcParams &p, int64_t t, int64_t n, float e_n, float bias,
-                                               const float (&acc)[8])
+__device__ __forceinline__ void store_outputs8(const TcParams &p, int64_t t, int64_t n, float e_n, float z_n,
+                                               float bias, const float (&acc)[8])
 {
-    EpiOperands eo[FORM == kEpi ? 8 : 1];
-    if constexpr (FORM == kEpi) {
+    EpiOperands eo[FORM == kPlain ? 1 : 8];
+    float2 rc[FORM == kQ8 ? 8 : 1];
+    if constexpr (FORM != kPlain) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if constexpr (FORM == kQ8)
+                rc[j] = t + j < p.M ? __ldcg(p.rowc + t + j) : make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             eo[j].bias = bias;
@@ -279,7 +299,9 @@ __device__ __forceinline__ void store_outputs8(const TcParams &p, int64_t t, int
         if (t + j >= p.M)
             continue;
         float v = e_n * acc[j];
-        if constexpr (FORM == kEpi)
+        if constexpr (FORM == kQ8)
+            v = e_n * rc[j].x * (acc[j] - z_n * rc[j].y);
+        if constexpr (FORM != kPlain)
             v = epi_apply(p.epi, v, eo[j]);
         p.y[(t + j) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
     }
@@ -290,9 +312,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_codes,
                const __grid_constant__ CUtensorMap tm_bt, const __grid_constant__ CUtensorMap tm_v, TcParams p)
 {
-    constexpr int STAGES = tc_stages(BN);
+    constexpr int BK = tc_bk(FORM);
+    constexpr int C_BYTES = tc_c_bytes(FORM);
+    constexpr int STAGES = tc_stages(BN, FORM);
     constexpr int B_BYTES = tc_b_bytes(BN);
-    constexpr int STAGE_BYTES = tc_stage_bytes(BN);
+    constexpr int STAGE_BYTES = tc_stage_bytes(BN, FORM);
+    constexpr int SUB = 256 / BK;   // stages per tiled code block
     constexpr int TMEM_COLS = 2 * BN;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[3 * STAGES + 5];
@@ -364,9 +389,9 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     if (st < p.n_main) {
                         mbar_expect_tx(full, B_BYTES + C_BYTES);
                         tma_load_2d(sb + A_BYTES, &tm_x, st * BK, t0, full);
-                        const int blk = (n0 / 64) * p.kchunks + st / 4;
-                        tma_load_4d(sb + A_BYTES + B_BYTES, &tm_codes, 0, st & 3, 0, blk, full);
-                        tma_load_4d(sb + A_BYTES + B_BYTES + C_BYTES / 2, &tm_codes, 0, st & 3, 0, blk + p.kchunks,
+                        const int blk = (n0 / 64) * p.kchunks + st / SUB, sub = st % SUB;
+                        tma_load_4d(sb + A_BYTES + B_BYTES, &tm_codes, 0, sub, 0, blk, full);
+                        tma_load_4d(sb + A_BYTES + B_BYTES + C_BYTES / 2, &tm_codes, 0, sub, 0, blk + p.kchunks,
                                     full);
                     } else {
                         if (!v_seen) {
@@ -409,8 +434,9 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         if (lane == 0) {
+            const uint32_t ab = FORM == kQ8 ? 0u : (1u << 7) | (1u << 10);   // A, B: e4m3 or bf16
             const uint32_t idesc = (1u << 4)                    // D: f32
-                                   | (1u << 7) | (1u << 10)     // A, B: bf16
+                                   | ab
                                    | ((uint32_t)(BN >> 3) << 17)
                                    | ((uint32_t)(BM >> 4) << 24);
             const uint32_t idesc_tf32 = (1u << 4)               // D: f32
@@ -445,8 +471,14 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     const uint32_t sb = base + slot * STAGE_BYTES;
                     const uint64_t a_desc = smem_desc_sw128(sb), b_desc = smem_desc_sw128(sb + A_BYTES);
                     if (st < p.n_main) {
-                        for (int k = 0; k < BK / 16; ++k)
-                            mma_bf16(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, (i > 0 || k > 0) ? 1u : 0u);
+                        // 32 bytes of k an instruction
+                        for (int k = 0; k < ROW_BYTES / 32; ++k) {
+                            const uint32_t accumulate = (i > 0 || k > 0) ? 1u : 0u;
+                            if constexpr (FORM == kQ8)
+                                mma_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
+                            else
+                                mma_bf16(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
+                        }
                     } else {
                         // EC: 32 tf32 values of j per 128-byte row, 8 per instruction
                         const int rem = p.rp - (st - p.n_main) * 32;
@@ -481,6 +513,7 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const uint32_t zb = __bfloat16_as_ushort(__float2bfloat16_rn(-(float)(128u + p.z[n])));
             const uint32_t negz = live ? (zb | (zb << 16)) : 0u;
             const uint32_t mulz = live ? 0x3F803F80u : 0u;
+            const uint32_t nib = live ? 0x0F0F0F0Fu : 0u;
             bool ok = true;
             for (int ii = 0; ii < nst; ++ii, ++g) {
                 if ((g & 1u) != grp)
@@ -491,7 +524,26 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     ok = false;
                     break;
                 }
-                if (st < p.n_main) {
+                if (FORM == kQ8 && st < p.n_main) {
+                    uint8_t *sb = base_ptr + slot * STAGE_BYTES;
+                    const uint8_t *crow = sb + A_BYTES + B_BYTES + i * 64;
+                    uint8_t *arow = sb + i * 128;
+                    // code row i: 64 bytes (128 k), its four 16-byte pieces permuted by
+                    // row bits 1 and 2 (64-byte TMA swizzle, conflict-free reads)
+#pragma unroll
+                    for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(crow + ((c ^ ((i >> 1) & 3)) << 4));
+                        // 16 codes a store, eight a word: see nibbles_to_e4m3
+                        uint4 o;
+                        nibbles_to_e4m3(w.x, nib, o.x, o.y);
+                        nibbles_to_e4m3(w.y, nib, o.z, o.w);
+                        *reinterpret_cast<uint4 *>(arow + (((2 * c) ^ (i & 7)) << 4)) = o;
+                        nibbles_to_e4m3(w.z, nib, o.x, o.y);
+                        nibbles_to_e4m3(w.w, nib, o.z, o.w);
+                        *reinterpret_cast<uint4 *>(arow + (((2 * c + 1) ^ (i & 7)) << 4)) = o;
+                    }
+                    fence_proxy_async_smem();
+                } else if (st < p.n_main) {
                     uint8_t *sb = base_ptr + slot * STAGE_BYTES;
                     // code row i: 32 bytes (64 k), its two 16-byte halves swapped in rows
                     // with bit 2 set (32-byte TMA swizzle, conflict-free reads)
@@ -532,7 +584,29 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const int64_t n = (int64_t)(tile / p.n_ttiles) * BM + row;
             const float sn = p.s[n];
             const float e_n = sn != 0.0f ? sn : 1.0f;   // the EC operand was divided by it
-            const float bias = FORM == kEpi && p.epi.bias && n < p.N ? bf16_lo(__ldg(p.epi.bias + n)) : 0.f;
+            const float bias = FORM != kPlain && p.epi.bias && n < p.N ? bf16_lo(__ldg(p.epi.bias + n)) : 0.f;
+            const float z_n = FORM == kQ8 && sn != 0.0f ? (float)p.z[n] : 0.f;
+            if (FORM != kPlain && p.ksplit == 1) {
+                // 16 columns at a time: the operands of eight outputs take the registers
+#pragma unroll 1
+                for (int c = 0; c < BN / 16; ++c) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * q) << 16) + buf * BN + 16 * c, r);
+                    if (n < p.N) {
+#pragma unroll
+                        for (int j0 = 0; j0 < 16; j0 += 8) {
+                            float a[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                a[j] = __uint_as_float(r[j0 + j]);
+                            store_outputs8<FORM>(p, t0 + 16 * c + j0, n, e_n, z_n, bias, a);
+                        }
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(tempty0 + 8 * buf);
+                continue;
+            }
             if (p.ksplit == 1) {
 #pragma unroll 1
                 for (int c = 0; c < BN / 32; ++c) {
@@ -545,7 +619,7 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 a[j] = __uint_as_float(r[j0 + j]);
-                            store_outputs8<FORM>(p, t0 + 32 * c + j0, n, e_n, bias, a);
+                            store_outputs8<FORM>(p, t0 + 32 * c + j0, n, e_n, z_n, bias, a);
                         }
                     }
                 }
@@ -593,7 +667,7 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                             v[jj] += w[jj];
                     }
                     if (n < p.N)
-                        store_outputs8<FORM>(p, t0 + j0, n, e_n, bias, v);
+                        store_outputs8<FORM>(p, t0 + j0, n, e_n, z_n, bias, v);
                 }
                 if (q == 0 && lane == 0)
                     p.counters[tile] = 0u;   // for the next forward
@@ -674,6 +748,13 @@ cudaError_t tc_prepare(const Packed &pk, TcWork &w)
     const uint32_t box[4] = {8, 1, 64, 1};
     cudaError_t e = make_map_nd(&m->codes, pk.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, dims, strides, box,
                                 CU_TENSOR_MAP_SWIZZLE_32B);
+    if (e == cudaSuccess) {
+        const uint64_t dims2[4] = {16, 2, 64, dims[3]};
+        const uint64_t strides2[3] = {64, 128, 8192};
+        const uint32_t box2[4] = {16, 1, 64, 1};
+        e = make_map_nd(&m->codes128, pk.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, dims2, strides2, box2,
+                        CU_TENSOR_MAP_SWIZZLE_64B);
+    }
     if (e == cudaSuccess && pk.r > 0)
         e = make_map(&m->g, pk.G, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)pk.Kp, (uint64_t)pk.R1p, 64,
                      (uint32_t)pk.R1p, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -701,7 +782,8 @@ TcFn tc_fn(int BN)
 
 cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                       const TcWork &w, int *status, bool zero_wait_budget, cudaStream_t st, int num_sms,
-                      unsigned *v_ready, unsigned v_expected, const Epilogue *epi)
+                      unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
+                      const float2 *rowc)
 {
     if (M <= 0)
         return cudaSuccess;
@@ -717,8 +799,13 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
     // up to 256), so that small batches do not run 256-wide MMAs on zero rows
     const int BN = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));
     CUtensorMap tm_x, tm_v;
-    cudaError_t e = make_map(&tm_x, x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)pk.K, (uint64_t)M, BK,
-                             (uint32_t)BN, CU_TENSOR_MAP_SWIZZLE_128B);
+    const int BK = tc_bk(form);
+    const uint64_t xd[2] = {(uint64_t)pk.K, (uint64_t)M};
+    const uint64_t xst[1] = {(uint64_t)ldx * (uint64_t)(ROW_BYTES / BK)};
+    const uint32_t xb[2] = {(uint32_t)BK, (uint32_t)BN};
+    cudaError_t e = make_map_nd(&tm_x, x, form == kQ8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                2, xd, xst, xb, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess)
         return e;
     const bool use_ec = ec && pk.r > 0;
@@ -755,10 +842,10 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
     p.v_ready = use_ec ? v_ready : nullptr;
     p.v_expected = v_expected;
 
-    if (epi)
-        p.epi = *epi;
-    const TcFn fn = epi ? tc_fn<kEpi>(BN) : tc_fn<kPlain>(BN);
-    const int smem = tc_smem_bytes(BN);
+    p.epi = epi;
+    p.rowc = rowc;
+    const TcFn fn = form == kQ8 ? tc_fn<kQ8>(BN) : (form == kEpi ? tc_fn<kEpi>(BN) : tc_fn<kPlain>(BN));
+    const int smem = tc_smem_bytes(BN, form);
     e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess)
         return e;
@@ -773,7 +860,8 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const CUtensorMap &bt = use_ec ? m->bt : m->codes;
-    return cudaLaunchKernelEx(&cfg, fn, tm_x, m->codes, bt, tm_v, p);
+    const CUtensorMap &codes = form == kQ8 ? m->codes128 : m->codes;
+    return cudaLaunchKernelEx(&cfg, fn, tm_x, codes, bt, tm_v, p);
 }
 
 }  // namespace spear

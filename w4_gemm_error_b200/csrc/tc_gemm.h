@@ -15,6 +15,23 @@ struct TcWork {
     int n_counters = 0;
 };
 
+// Workspace of the 8-bit form's prepass.
+struct PrepassQ8Work {
+    float2 *rowc = nullptr;      // [max_M]
+    float *part = nullptr;       // split-K partials
+    size_t part_floats = 0;
+    unsigned *counters = nullptr;
+    int n_counters = 0;
+};
+cudaError_t prepass_q8_alloc(const Packed &pk, int64_t max_M, int num_sms, PrepassQ8Work &w);
+void prepass_q8_free(PrepassQ8Work &w);
+// rowc and (with `ec`) v of M tokens of e4m3 activations, rows ldx apart; see
+// prepass_q8.cu.  `ready` (may be null) is counted *expected times in all, once
+// per token tile when its v and rowc are written.
+cudaError_t launch_prepass_q8(const Packed &pk, const void *xq, int64_t ldx, const float *xs, int64_t M, bool ec,
+                              float *v, const PrepassQ8Work &w, cudaStream_t st, int num_sms, unsigned *ready,
+                              unsigned *expected);
+
 bool tc_available(const Packed &pk);
 cudaError_t tc_alloc(const Packed &pk, int64_t max_M, int num_sms, TcWork &w);
 void tc_free(TcWork &w);
@@ -30,9 +47,11 @@ cudaError_t launch_tc_prepass(const Packed &pk, const void *x, int64_t M, float 
 // without waiting for its predecessor, which must be a prepass that counts
 // v_expected completions into v_ready[0] and starts its dependents only once x is
 // complete; v_ready[0..1] are zero between calls.
-// epi (may be null): bias, activation, multiplier and residual of the outputs.
+// form and epi: see epilogue.cuh; rows of x are ldx elements apart; rowc: the
+// prepass's per-token pair of form kQ8 (null otherwise).
 cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                       const TcWork &w, int *status, bool zero_wait_budget, cudaStream_t st, int num_sms,
-                      unsigned *v_ready, unsigned v_expected, const Epilogue *epi = nullptr);
+                      unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
+                      const float2 *rowc);
 
 }  // namespace spear
