@@ -230,7 +230,11 @@ cudaError_t prepass_q8_alloc(const Packed &pk, int64_t max_M, int num_sms, Prepa
         worst = std::max(worst, part_floats(pk, i * kTok, num_sms));
     w.part_floats = worst;
     w.n_counters = (int)tiles;
-    cudaError_t e = cudaMalloc(&w.rowc, (size_t)max_M * sizeof(float2));
+    // whole chunks of 32 tokens, zero where no token is (a copy of a chunk reads all of it)
+    const size_t rowc_bytes = (size_t)((max_M + 31) / 32 * 32) * sizeof(float2);
+    cudaError_t e = cudaMalloc(&w.rowc, rowc_bytes);
+    if (e == cudaSuccess)
+        e = cudaMemset(w.rowc, 0, rowc_bytes);
     if (e == cudaSuccess && worst)
         e = cudaMalloc(&w.part, worst * sizeof(float));
     if (e == cudaSuccess)
