@@ -21,6 +21,18 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -359,25 +371,15 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem, uint32_t rank)
     return r;
 }
 
-// Arrive (release, cluster scope) on the barrier of this offset in CTA `rank`.
+// Arrive on the barrier of this offset in CTA `rank` of the cluster.  The
+// release is of CTA scope (the default): what it orders here is this SM's
+// shared and tensor memory, made visible by fence.proxy.async or
+// tcgen05.fence before the arrive and read by this SM's own tensor core or
+// overwritten by it.  A release of cluster scope waits for every load in
+// flight of the thread and took 1000 to 1700 cycles a stage.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar, uint32_t rank)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, rank))
-                 : "memory");
-}
-
-// As mbar_try_wait_sleep, acquiring at cluster scope.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity, uint32_t ns)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(ns)
-        : "memory");
-    return ok != 0;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, rank)) : "memory");
 }
 
 // Volatile (kept after the cluster barrier that orders it against the

@@ -796,8 +796,8 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
         return cudaMemcpyAsync(status, &bits, sizeof(int), cudaMemcpyHostToDevice, st);
     }
     if (form != kPlain && M >= kPairMinTokens)
-        return launch_tc_pair(pk, x, y, M, v, ec, form == kQ8 ? m->codes128 : m->codes, m->bt, status, st, num_sms,
-                              v_ready, v_expected, form, epi, ldx, rowc);
+        return launch_tc_pair(pk, x, y, M, v, ec, &m->bt, status, st, num_sms, v_ready, v_expected, form,
+                              epi, ldx, rowc);
     // token tile: the narrowest of 32, 64, 128, 256 that holds M (one tile row of tokens
     // up to 256), so that small batches do not run 256-wide MMAs on zero rows
     const int BN = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));

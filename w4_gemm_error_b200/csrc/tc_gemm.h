@@ -55,11 +55,10 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
                       const float2 *rowc);
 
 // The forms kEpi and kQ8 from kPairMinTokens tokens on (tc_pair.cu; launch_tc
-// takes it).  codes, bt: the tensor maps of launch_tc; rowc holds whole chunks of
-// 32 tokens.
+// takes it).  bt: the tensor map of B^T/e; rowc holds whole chunks of 32 tokens.
 constexpr int64_t kPairMinTokens = 129;
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
-                           const CUtensorMap &codes, const CUtensorMap &bt, int *status, cudaStream_t st, int num_sms,
+                           const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,
                            unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
                            const float2 *rowc);
 

@@ -15,18 +15,27 @@
 // so each SM stages half the activations for the same products.
 //
 // Roles in each CTA (20 warps):
-//   warp 0       TMA producer of the stages: its 128 tokens of x and its 128
-//                rows of codes (EC stages: v and B^T/e instead)
-//   warp 1       TMEM allocation; in the pair's first CTA the one thread that
-//                issues the MMAs of both
+//   warp 0       TMA producer of the stages: its 128 tokens of x (EC stages: v
+//                and B^T/e)
+//   warp 1       TMEM allocation; in the pair's first CTA the issuer of the
+//                MMAs of both
 //   warp 2       loader of the epilogue's operands (multiplier, residual and
 //                per-token constants) into slots of 32 tokens x 128 channels
 //   warps 4-11   epilogue, two sets of four warps (each warp its 32 TMEM
 //                lanes) taking alternate slots: accumulator from TMEM, the
 //                formula above, y into the slot (over the residual, element by
 //                element) and from there to HBM by one TMA store a slot
-//   warps 12-19  dequantisers, two groups of four taking alternate stages,
-//                one weight row a thread
+//   warps 12-19  dequantisers, two groups of four taking alternate stages:
+//                codes from global memory into registers two stages of the
+//                group ahead, from there into the stage as MMA operands
+// The codes never pass through shared memory before they are dequantised, so
+// that the ring of stages (5, or 6 without a multiplier) is deep enough to
+// cover the latency from a TMA request to the MMA that frees its stage: with
+// four stages that held the codes too, a 128-k stage took 1200 cycles instead
+// of the 512 of its MMAs.  The producer and the MMA issuer run as whole warps
+// with one elected lane in the asynchronous instructions, so that addresses
+// and descriptors stay in uniform registers (issued from a single-lane branch,
+// the four MMAs of a stage alone cost about 400 cycles).
 // Two accumulators of 256 columns in TMEM: the epilogue of a tile overlaps the
 // main loop of the next.  Every wait is bounded (about a second); one that runs
 // out sets the handle's status word and the kernel winds down.
@@ -45,20 +54,21 @@ constexpr int BN = 256;                 // tokens of a pair (128 staged by each 
 constexpr int ROW_BYTES = 128;
 constexpr int A_BYTES = BM * ROW_BYTES;
 constexpr int B_BYTES = (BN / 2) * ROW_BYTES;
-constexpr int STAGES = 4;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int MAX_STAGES = 6;
 constexpr int CHUNK = 32;               // tokens of an epilogue slot
 constexpr int NSLOT = 4;
-constexpr int SLOT_BYTES = 2 * CHUNK * BM * 2;   // multiplier, then residual / y
+constexpr int HALF_SLOT = CHUNK * BM * 2;   // residual / y; a second one for the multiplier
 constexpr int ROWC_BYTES = CHUNK * 8;
 constexpr int THREADS = 640;
 constexpr int EPI_WARP = 4, DEQ_WARP = 12;
 
 __host__ __device__ constexpr int pair_bk(int form) { return form == kQ8 ? 128 : 64; }
-__host__ __device__ constexpr int pair_c_bytes(int form) { return BM * pair_bk(form) / 2; }
-__host__ __device__ constexpr int pair_stage_bytes(int form) { return A_BYTES + B_BYTES + pair_c_bytes(form); }
-__host__ __device__ constexpr int pair_smem_bytes(int form)
+// Ring depth and shared memory with and without a multiplier in the slots.
+int pair_stages(bool mul) { return mul ? 5 : 6; }
+int pair_smem_bytes(bool mul)
 {
-    return STAGES * pair_stage_bytes(form) + NSLOT * (SLOT_BYTES + ROWC_BYTES) + 1024;
+    return pair_stages(mul) * STAGE_BYTES + NSLOT * (HALF_SLOT * (mul ? 2 : 1) + ROWC_BYTES) + 1024;
 }
 
 struct PairParams {
@@ -66,6 +76,8 @@ struct PairParams {
     int kchunks;             // Kp / 256
     int n_main, n_ec, rp;    // stages of the main loop and of the EC; columns of v
     int n_ttiles, n_units;
+    int stages;
+    const uint8_t *codes;    // the tiled codes (Packed::codes)
     const float *s;
     const uint8_t *z;
     int *status;
@@ -74,23 +86,6 @@ struct PairParams {
     Epilogue epi;
     const float2 *rowc;      // form kQ8: as TcParams::rowc, padded to whole chunks
 };
-
-// Bounded wait with cluster scope (arrivals from the other CTA of the pair).
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                                  int *status)
-{
-    const long long t0 = clock64();
-    while (!mbar_try_wait_cluster(bar, parity, kWaitSleepNs)) {
-        if (*abort_flag)
-            return false;
-        if (clock64() - t0 > kWaitBudgetCycles) {
-            *abort_flag = 1;
-            atomicOr(status, kStatusTimeout);
-            return false;
-        }
-    }
-    return true;
-}
 
 // Bounded wait until the prepass has counted everything it writes.
 __device__ __forceinline__ bool wait_prepass(const PairParams &p, volatile int *abort_flag)
@@ -108,47 +103,92 @@ __device__ __forceinline__ bool wait_prepass(const PairParams &p, volatile int *
     return true;
 }
 
+// A warp's wait: every lane waits, all learn the same outcome.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
 // One slot's outputs of this thread: channel n (row `row` of the CTA), the 32
 // tokens of the chunk, the accumulator in acc.  mul and y are its columns of
-// the slot's two halves ([32 tokens][128 channels] bf16).
-template <int FORM, int ACT>
+// [32 tokens][128 channels] bf16.  Eight tokens at a time: every shared-memory
+// read of a group comes before its first store.
+template <int FORM, int ACT, bool MUL, bool RES>
 __device__ __forceinline__ void emit_chunk(const uint32_t (&acc)[CHUNK], float e_n, float z_n, float bias,
-                                           const uint16_t *mul, uint16_t *y, const float2 *rc, bool has_mul,
-                                           bool has_res)
+                                           const uint16_t *mul, uint16_t *y, const float4 *rc)
 {
 #pragma unroll
-    for (int j = 0; j < CHUNK; ++j) {
-        float v = __uint_as_float(acc[j]);
-        if constexpr (FORM == kQ8) {
-            const float2 c = rc[j];
-            v = c.x * e_n * (v - z_n * c.y);
-        } else {
-            v = e_n * v;
+    for (int j0 = 0; j0 < CHUNK; j0 += 8) {
+        float v[8], m[8], r[8];
+        float4 c[4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (FORM == kQ8 && (j & 1) == 0)
+                c[j / 2] = rc[(j0 + j) / 2];   // the constants of two tokens
+            m[j] = MUL ? bf16_lo(mul[(j0 + j) * BM]) : 1.f;
+            r[j] = RES ? bf16_lo(y[(j0 + j) * BM]) : 0.f;
         }
-        v = activate(v + bias, ACT);
-        if (has_mul)
-            v *= bf16_lo(mul[j * BM]);
-        if (has_res)
-            v += bf16_lo(y[j * BM]);
-        y[j * BM] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = __uint_as_float(acc[j0 + j]);
+            if constexpr (FORM == kQ8) {
+                const float cx = (j & 1) ? c[j / 2].z : c[j / 2].x, cy = (j & 1) ? c[j / 2].w : c[j / 2].y;
+                v[j] = e_n * cx * (v[j] - z_n * cy);
+            } else {
+                v[j] *= e_n;
+            }
+            v[j] = activate(v[j] + bias, ACT);
+            if (MUL)
+                v[j] *= m[j];
+            if (RES)
+                v[j] += r[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const uint32_t two = pack_bf16x2(v[j], v[j + 1]);
+            y[(j0 + j) * BM] = (uint16_t)two;
+            y[(j0 + j + 1) * BM] = (uint16_t)(two >> 16);
+        }
     }
 }
 
+template <int FORM, int ACT>
+__device__ __forceinline__ void emit_chunk_of(const uint32_t (&acc)[CHUNK], float e_n, float z_n, float bias,
+                                              const uint16_t *mul, uint16_t *y, const float4 *rc, bool has_mul,
+                                              bool has_res)
+{
+    if (has_mul)
+        has_res ? emit_chunk<FORM, ACT, true, true>(acc, e_n, z_n, bias, mul, y, rc)
+                : emit_chunk<FORM, ACT, true, false>(acc, e_n, z_n, bias, mul, y, rc);
+    else
+        has_res ? emit_chunk<FORM, ACT, false, true>(acc, e_n, z_n, bias, mul, y, rc)
+                : emit_chunk<FORM, ACT, false, false>(acc, e_n, z_n, bias, mul, y, rc);
+}
+
+// A dequantiser thread's codes of one stage: `kPieces` 16-byte pieces, lanes
+// side by side in a row's piece so that a warp's load is whole 32-byte sectors.
+// Form kQ8 (64 bytes a row): piece lane % 4 of rows lane / 4 + 8 j; kEpi
+// (32 bytes a row): piece lane % 2 of rows lane / 2 + 16 j.
+template <int FORM>
+struct Codes {
+    static constexpr int kLanes = FORM == kQ8 ? 4 : 2;    // lanes a row
+    static constexpr int kPieces = FORM == kQ8 ? 4 : 2;   // pieces (rows) a thread
+    uint4 w[kPieces];
+};
+
 template <int FORM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_codes,
-               const __grid_constant__ CUtensorMap tm_bt, const __grid_constant__ CUtensorMap tm_v,
+tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_bt, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_mul, const __grid_constant__ CUtensorMap tm_res,
                const __grid_constant__ CUtensorMap tm_y, PairParams p)
 {
     constexpr int BK = pair_bk(FORM);
-    constexpr int C_BYTES = pair_c_bytes(FORM);
-    constexpr int STAGE_BYTES = pair_stage_bytes(FORM);
     constexpr int SUB = 256 / BK;
     constexpr int GROUP_WARPS = 4;
     extern __shared__ uint8_t smem_raw[];
     // full, ready and empty of each stage; accumulator full and empty; slot full and empty; drain
-    __shared__ __align__(8) uint64_t bars[3 * STAGES + 4 + 2 * NSLOT + 1];
+    __shared__ __align__(8) uint64_t bars[3 * MAX_STAGES + 4 + 2 * NSLOT + 1];
     __shared__ uint32_t tmem_base_slot;
     __shared__ volatile int abort_flag;
 
@@ -157,18 +197,22 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     uint8_t *const base_ptr = smem_raw + (base - smem_addr(smem_raw));
     const uint32_t rank = cluster_ctarank();
     const uint32_t full0 = smem_addr(&bars[0]);
-    const uint32_t ready0 = smem_addr(&bars[STAGES]);         // first CTA's: both CTAs' operands are staged
-    const uint32_t empty0 = smem_addr(&bars[2 * STAGES]);
-    const uint32_t tfull0 = smem_addr(&bars[3 * STAGES]);
-    const uint32_t tempty0 = smem_addr(&bars[3 * STAGES + 2]);   // first CTA's: both epilogues are done
-    const uint32_t sfull0 = smem_addr(&bars[3 * STAGES + 4]);
-    const uint32_t sempty0 = smem_addr(&bars[3 * STAGES + 4 + NSLOT]);
-    const uint32_t drain = smem_addr(&bars[3 * STAGES + 4 + 2 * NSLOT]);
-    constexpr uint32_t kSlots = STAGES * STAGE_BYTES, kRowc = kSlots + NSLOT * SLOT_BYTES;
+    const uint32_t ready0 = smem_addr(&bars[MAX_STAGES]);         // first CTA's: both CTAs' operands are staged
+    const uint32_t empty0 = smem_addr(&bars[2 * MAX_STAGES]);
+    const uint32_t tfull0 = smem_addr(&bars[3 * MAX_STAGES]);
+    const uint32_t tempty0 = smem_addr(&bars[3 * MAX_STAGES + 2]);   // first CTA's: both epilogues are done
+    const uint32_t sfull0 = smem_addr(&bars[3 * MAX_STAGES + 4]);
+    const uint32_t sempty0 = smem_addr(&bars[3 * MAX_STAGES + 4 + NSLOT]);
+    const uint32_t drain = smem_addr(&bars[3 * MAX_STAGES + 4 + 2 * NSLOT]);
+    const uint32_t S = (uint32_t)p.stages;
+    const bool has_mul = p.epi.mul != nullptr, has_res = p.epi.residual != nullptr;
+    // byte offsets: residual / y halves of the slots, multiplier halves, per-token constants
+    const uint32_t o_y = S * STAGE_BYTES, o_mul = o_y + NSLOT * HALF_SLOT;
+    const uint32_t o_rowc = o_mul + (has_mul ? NSLOT * HALF_SLOT : 0);
 
     if (tid == 0) {
         abort_flag = 0;
-        for (int s = 0; s < STAGES; ++s) {
+        for (uint32_t s = 0; s < S; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(ready0 + 8 * s, 2 * GROUP_WARPS);
             mbar_init(empty0 + 8 * s, 1);
@@ -203,97 +247,116 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            if (!p.v_ready)
-                pdl_wait();   // x and v come from earlier kernels in the stream
-            bool v_seen = p.v_ready == nullptr;
-            uint32_t g = 0;
-            bool ok = true;
-            for (int u = cluster; u < p.n_units && ok; u += n_clusters) {
-                const int t0 = (u % p.n_ttiles) * BN + (int)rank * (BN / 2);
-                const int n0 = (u / p.n_ttiles) * 2 * BM + (int)rank * BM;
-                for (int i = 0; i < nst; ++i, ++g) {
-                    const uint32_t slot = g % STAGES, phase = (g / STAGES) & 1;
-                    if (!mbar_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status)) {
+        const bool elected = elect_one();
+        if (!p.v_ready)
+            pdl_wait();   // x and v come from earlier kernels in the stream
+        bool v_seen = p.v_ready == nullptr;
+        uint32_t slot = 0, phase = 0, issued = 0;
+        bool ok = true;
+        for (int u = cluster; u < p.n_units && ok; u += n_clusters) {
+            const int t0 = (u % p.n_ttiles) * BN + (int)rank * (BN / 2);
+            const int n0 = (u / p.n_ttiles) * 2 * BM + (int)rank * BM;
+            for (int i = 0; i < nst; ++i) {
+                if (!warp_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sb = base + slot * STAGE_BYTES, full = full0 + 8 * slot;
+                if (i < p.n_main) {
+                    if (elected) {
+                        mbar_expect_tx(full, B_BYTES);
+                        tma_load_2d(sb + A_BYTES, &tm_x, i * BK, t0, full);
+                    }
+                } else {
+                    if (!v_seen && !__all_sync(0xffffffffu, wait_prepass(p, &abort_flag))) {
                         ok = false;
                         break;
                     }
-                    const uint32_t sb = base + slot * STAGE_BYTES, full = full0 + 8 * slot;
-                    if (i < p.n_main) {
-                        mbar_expect_tx(full, B_BYTES + C_BYTES);
-                        tma_load_2d(sb + A_BYTES, &tm_x, i * BK, t0, full);
-                        const int blk = (n0 / 64) * p.kchunks + i / SUB, sub = i % SUB;
-                        tma_load_4d(sb + A_BYTES + B_BYTES, &tm_codes, 0, sub, 0, blk, full);
-                        tma_load_4d(sb + A_BYTES + B_BYTES + C_BYTES / 2, &tm_codes, 0, sub, 0, blk + p.kchunks,
-                                    full);
-                    } else {
-                        if (!v_seen && !wait_prepass(p, &abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        v_seen = true;
+                    v_seen = true;
+                    if (elected) {
                         const int e = i - p.n_main;   // 32 tf32 values of j a stage
                         mbar_expect_tx(full, A_BYTES + B_BYTES);
                         tma_load_2d(sb, &tm_bt, e * 32, n0, full);
                         tma_load_2d(sb + A_BYTES, &tm_v, e * 32, t0, full);
                     }
                 }
+                ++issued;
+                if (++slot == S) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
-            // do not leave while copies this CTA issued may still land (the
-            // dequantisers waited for every stage unless a wait gave up)
-            if (abort_flag)
-                for (uint32_t k = 0; k < STAGES && k < g; ++k)
-                    mbar_wait_final(full0 + 8 * ((g - 1 - k) % STAGES), ((g - 1 - k) / STAGES) & 1);
-            // early start: this grid completes only after its predecessor
-            if (p.v_ready)
-                pdl_wait();
         }
+        // do not leave while copies this CTA issued may still land (the
+        // dequantisers waited for every stage unless a wait gave up)
+        if (abort_flag)
+            for (uint32_t k = 0; k < S && k < issued; ++k) {
+                const uint32_t g = issued - 1 - k;
+                mbar_wait_final(full0 + 8 * (g % S), (g / S) & 1);
+            }
+        // early start: this grid completes only after its predecessor
+        if (p.v_ready)
+            pdl_wait();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer of the pair
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const bool elected = elect_one();
             const uint32_t shape = ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(2 * BM >> 4) << 24) | (1u << 4);
             const uint32_t idesc = shape | (FORM == kQ8 ? 0u : (1u << 7) | (1u << 10));
             const uint32_t idesc_tf32 = shape | (2u << 7) | (2u << 10);
-            uint32_t g = 0;
+            const uint64_t a0 = smem_desc_sw128(base), b0 = smem_desc_sw128(base + A_BYTES);
+            uint32_t slot = 0, phase = 0;
             int lt = 0;
             bool ok = true;
             for (int u = cluster; u < p.n_units && ok; u += n_clusters, ++lt) {
                 const uint32_t buf = lt & 1;
-                if (!mbar_wait_cluster(tempty0 + 8 * buf, ((lt >> 1) & 1) ^ 1, &abort_flag, p.status))
+                if (!warp_wait(tempty0 + 8 * buf, ((lt >> 1) & 1) ^ 1, &abort_flag, p.status))
                     break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * BN;
-                for (int i = 0; i < nst; ++i, ++g) {
-                    const uint32_t slot = g % STAGES, phase = (g / STAGES) & 1;
-                    if (!mbar_wait_cluster(ready0 + 8 * slot, phase, &abort_flag, p.status)) {
+                for (int i = 0; i < nst; ++i) {
+                    if (!warp_wait(ready0 + 8 * slot, phase, &abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sb = base + slot * STAGE_BYTES;
-                    const uint64_t a_desc = smem_desc_sw128(sb), b_desc = smem_desc_sw128(sb + A_BYTES);
+                    const uint64_t a_desc = a0 + slot * (STAGE_BYTES >> 4), b_desc = b0 + slot * (STAGE_BYTES >> 4);
                     if (i < p.n_main) {
-                        // 32 bytes of k an instruction
-                        for (int k = 0; k < ROW_BYTES / 32; ++k) {
-                            const uint32_t accumulate = (i > 0 || k > 0) ? 1u : 0u;
-                            if constexpr (FORM == kQ8)
-                                mma2_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
-                            else
-                                mma2_bf16(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
+                        if (elected) {
+                            // 32 bytes of k an instruction
+#pragma unroll
+                            for (int k = 0; k < ROW_BYTES / 32; ++k) {
+                                const uint32_t accumulate = (i > 0 || k > 0) ? 1u : 0u;
+                                if constexpr (FORM == kQ8)
+                                    mma2_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
+                                else
+                                    mma2_bf16(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
+                            }
+                            mma2_commit_both(empty0 + 8 * slot);
                         }
                     } else {
                         const int rem = p.rp - (i - p.n_main) * 32;
                         const int ksteps = (rem < 32 ? rem : 32) / 8;
-                        for (int k = 0; k < ksteps; ++k)
-                            mma2_tf32(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc_tf32, 1u);
+                        if (elected) {
+                            for (int k = 0; k < ksteps; ++k)
+                                mma2_tf32(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc_tf32, 1u);
+                            mma2_commit_both(empty0 + 8 * slot);
+                        }
                     }
-                    mma2_commit_both(empty0 + 8 * slot);
+                    __syncwarp();
+                    if (++slot == S) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
                 }
-                if (ok)
+                if (ok && elected)
                     mma2_commit_both(tfull0 + 8 * buf);
+                __syncwarp();
             }
-            // every MMA this thread issued is complete before TMEM is released
-            mma2_commit(drain);
+            // every MMA this warp issued is complete before TMEM is released
+            if (elected)
+                mma2_commit(drain);
+            __syncwarp();
             mbar_wait_final(drain, 0);
         }
     } else if (warp == 2) {
@@ -304,7 +367,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 pdl_wait();
             uint32_t g = 0;
             bool ok = true;
-            const uint32_t bytes = (p.epi.mul ? CHUNK * BM * 2u : 0u) + (p.epi.residual ? CHUNK * BM * 2u : 0u) +
+            const uint32_t bytes = (has_mul ? HALF_SLOT : 0u) + (has_res ? HALF_SLOT : 0u) +
                                    (FORM == kQ8 ? (uint32_t)ROWC_BYTES : 0u);
             for (int u = cluster; u < p.n_units && ok; u += n_clusters) {
                 const int t0 = (u % p.n_ttiles) * BN;
@@ -317,7 +380,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = sfull0 + 8 * slot, dst = base + kSlots + slot * SLOT_BYTES;
+                    const uint32_t bar = sfull0 + 8 * slot;
                     if (bytes == 0) {
                         mbar_arrive(bar);
                         continue;
@@ -328,12 +391,12 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     }
                     ready = true;
                     mbar_expect_tx(bar, bytes);
-                    if (p.epi.mul)
-                        tma_load_2d(dst, &tm_mul, n0, t0 + c * CHUNK, bar);
-                    if (p.epi.residual)
-                        tma_load_2d(dst + SLOT_BYTES / 2, &tm_res, n0, t0 + c * CHUNK, bar);
+                    if (has_mul)
+                        tma_load_2d(base + o_mul + slot * HALF_SLOT, &tm_mul, n0, t0 + c * CHUNK, bar);
+                    if (has_res)
+                        tma_load_2d(base + o_y + slot * HALF_SLOT, &tm_res, n0, t0 + c * CHUNK, bar);
                     if (FORM == kQ8)
-                        bulk_load(base + kRowc + slot * ROWC_BYTES, p.rowc + t0 + c * CHUNK, ROWC_BYTES, bar);
+                        bulk_load(base + o_rowc + slot * ROWC_BYTES, p.rowc + t0 + c * CHUNK, ROWC_BYTES, bar);
                 }
             }
             // (the epilogue waited for every slot unless a wait gave up)
@@ -347,7 +410,6 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         const int q = warp & 3, set = (warp - EPI_WARP) >> 2;
         const int row = 32 * q + lane;
         const bool storer = q == 0 && lane == 0;
-        const bool has_mul = p.epi.mul != nullptr, has_res = p.epi.residual != nullptr;
         uint32_t g = 0;
         int lt = 0, stores = 0;
         // a wait that gives up ends this warp's waits and stores, but not its
@@ -372,23 +434,30 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 __syncwarp();
                 uint32_t acc[CHUNK];
                 tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(32 * q) << 16) + buf * BN + CHUNK * c, acc);
-                uint8_t *const sp = base_ptr + kSlots + slot * SLOT_BYTES;
-                const uint16_t *mul = reinterpret_cast<const uint16_t *>(sp) + row;
-                uint16_t *y = reinterpret_cast<uint16_t *>(sp + SLOT_BYTES / 2) + row;
-                const float2 *rc = reinterpret_cast<const float2 *>(base_ptr + kRowc + slot * ROWC_BYTES);
+                const uint16_t *mul = reinterpret_cast<const uint16_t *>(base_ptr + o_mul + slot * HALF_SLOT) + row;
+                uint16_t *y = reinterpret_cast<uint16_t *>(base_ptr + o_y + slot * HALF_SLOT) + row;
+                const float4 *rc = reinterpret_cast<const float4 *>(base_ptr + o_rowc + slot * ROWC_BYTES);
                 switch (p.epi.act) {
-                case kActRelu: emit_chunk<FORM, kActRelu>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res); break;
-                case kActSilu: emit_chunk<FORM, kActSilu>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res); break;
-                case kActGelu: emit_chunk<FORM, kActGelu>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res); break;
-                case kActGeluTanh:
-                    emit_chunk<FORM, kActGeluTanh>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res);
+                case kActRelu:
+                    emit_chunk_of<FORM, kActRelu>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res);
                     break;
-                default: emit_chunk<FORM, kActNone>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res); break;
+                case kActSilu:
+                    emit_chunk_of<FORM, kActSilu>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res);
+                    break;
+                case kActGelu:
+                    emit_chunk_of<FORM, kActGelu>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res);
+                    break;
+                case kActGeluTanh:
+                    emit_chunk_of<FORM, kActGeluTanh>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res);
+                    break;
+                default:
+                    emit_chunk_of<FORM, kActNone>(acc, e_n, z_n, bias, mul, y, rc, has_mul, has_res);
+                    break;
                 }
                 fence_proxy_async_smem();
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory");   // the set's four warps
                 if (storer && ok) {
-                    tma_store_2d(&tm_y, base + kSlots + slot * SLOT_BYTES + SLOT_BYTES / 2, n0, t0 + c * CHUNK);
+                    tma_store_2d(&tm_y, base + o_y + slot * HALF_SLOT, n0, t0 + c * CHUNK);
                     bulk_commit();
                     // the set's slot before this one has been read out: free it
                     if (stores++ > 0) {
@@ -405,72 +474,110 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (storer)
             bulk_wait_all();   // the stores are complete (and the slots read) before the CTA leaves
     } else if (warp >= DEQ_WARP) {
-        // ------------------------------------------------ dequantisers: group `grp` takes the stages g with
-        // g % 2 == grp, one weight row a thread
-        const uint32_t grp = (uint32_t)(warp - DEQ_WARP) / GROUP_WARPS;
-        const int i = 32 * (warp & 3) + lane;
-        uint32_t g = 0;
+        // ------------------------------------------------ dequantisers: group `grp` takes every second stage
+        using Piece = Codes<FORM>;
+        constexpr int kRowStep = 32 / Piece::kLanes;   // rows between a thread's pieces
+        const int grp = (warp - DEQ_WARP) / GROUP_WARPS, w = warp & 3;
+        const int piece = lane % Piece::kLanes, r0 = 32 * w + lane / Piece::kLanes;
+        // stages of this group in order: (unit, stage) pairs two stages apart
+        auto next = [&](int &u, int &st, int by) {
+            st += by;
+            while (st >= nst && u < p.n_units) {
+                st -= nst;
+                u += n_clusters;
+            }
+        };
+        // the codes do not depend on earlier kernels (no wait)
+        auto fetch = [&](int u, int st, Piece &c) {
+            const int nb = (u / p.n_ttiles) * 4 + (int)rank * 2 + (w >> 1);   // 64-row block of this warp's rows
+            const bool some = u < p.n_units && st < p.n_main && (int64_t)nb * 64 < p.Np;
+            const uint8_t *src = p.codes + (((int64_t)nb * p.kchunks + st / SUB) * 64 + (r0 & 63)) * 128 +
+                                 (st % SUB) * (BK / 2) + piece * 16;
+#pragma unroll
+            for (int j = 0; j < Piece::kPieces; ++j)
+                c.w[j] = some ? ld_stream(src + j * kRowStep * 128) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        int u = cluster, st = 0, fu, fst;
+        next(u, st, grp);
+        fu = u;
+        fst = st;
+        Piece ahead[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            fetch(fu, fst, ahead[b]);
+            next(fu, fst, 2);
+        }
+        uint32_t slot = (uint32_t)grp, phase = 0;   // (at least two stages)
+        int unit = -1;
+        uint32_t nib[Piece::kPieces], negz[Piece::kPieces];   // kEpi: multiplier and bias of a row's pairs
         bool ok = true;
-        for (int u = cluster; u < p.n_units && ok; u += n_clusters) {
-            const int64_t n = (int64_t)(u / p.n_ttiles) * 2 * BM + rank * BM + i;
-            // a row whose s is 0 has weights 0, whatever its codes (the epilogue scales it by 1)
-            const bool live = n < p.Np && p.s[n] != 0.0f;
-            const uint32_t negz = live ? dequant_bias<false>(p.z[n]) : 0u;
-            const uint32_t mulz = live ? 0x3F803F80u : 0u;
-            const uint32_t nib = live ? 0x0F0F0F0Fu : 0u;
-            for (int st = 0; st < nst; ++st, ++g) {
-                if ((g & 1u) != grp)
-                    continue;
-                const uint32_t slot = g % STAGES, phase = (g / STAGES) & 1;
-                if (!mbar_wait(full0 + 8 * slot, phase, &abort_flag, p.status)) {
-                    ok = false;
+        while (u < p.n_units && ok) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (u >= p.n_units || !ok)
                     break;
-                }
-                if (st < p.n_main) {
-                    uint8_t *sb = base_ptr + slot * STAGE_BYTES;
-                    uint8_t *arow = sb + i * ROW_BYTES;
-                    if constexpr (FORM == kQ8) {
-                        // 64 bytes of codes (128 k): four 16-byte pieces permuted by row bits 1 and 2
-                        // (64-byte TMA swizzle), each 32 e4m3 values
-                        const uint8_t *crow = sb + A_BYTES + B_BYTES + i * 64;
-                        uint4 w[4];
+                if (unit != u) {
+                    unit = u;
+                    const int64_t n0 = (int64_t)(u / p.n_ttiles) * 2 * BM + rank * BM + r0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            w[c] = *reinterpret_cast<const uint4 *>(crow + ((c ^ ((i >> 1) & 3)) << 4));
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint4 o;
-                            nibbles_to_e4m3(w[c].x, nib, o.x, o.y);
-                            nibbles_to_e4m3(w[c].y, nib, o.z, o.w);
-                            *reinterpret_cast<uint4 *>(arow + (((2 * c) ^ (i & 7)) << 4)) = o;
-                            nibbles_to_e4m3(w[c].z, nib, o.x, o.y);
-                            nibbles_to_e4m3(w[c].w, nib, o.z, o.w);
-                            *reinterpret_cast<uint4 *>(arow + (((2 * c + 1) ^ (i & 7)) << 4)) = o;
+                    for (int j = 0; j < Piece::kPieces; ++j) {
+                        // a row whose s is 0 has weights 0, whatever its codes (the epilogue scales it by 1)
+                        const int64_t n = n0 + j * kRowStep;
+                        const bool live = n < p.Np && __ldg(p.s + n) != 0.0f;
+                        if constexpr (FORM == kQ8) {
+                            nib[j] = live ? 0x0F0F0F0Fu : 0u;
+                        } else {
+                            nib[j] = live ? 0x3F803F80u : 0u;
+                            negz[j] = live ? dequant_bias<false>(__ldg(p.z + n)) : 0u;
                         }
-                    } else {
-                        // 32 bytes of codes (64 k): two 16-byte pieces swapped in rows with bit 2
-                        // set (32-byte TMA swizzle), each 32 bf16 values
-                        const uint8_t *crow = sb + A_BYTES + B_BYTES + i * 32;
+                    }
+                }
+                // the stage is free once the MMAs of its last round are done
+                ok = warp_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status);
+                if (ok && st < p.n_main) {
+                    uint8_t *const at = base_ptr + slot * STAGE_BYTES;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(crow + ((h ^ ((i >> 2) & 1)) << 4));
-                            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                    for (int j = 0; j < Piece::kPieces; ++j) {
+                        const int row = r0 + j * kRowStep;
+                        uint8_t *arow = at + row * ROW_BYTES;
+                        const uint4 c = ahead[b].w[j];
+                        if constexpr (FORM == kQ8) {
+                            // 32 codes: two 16-byte pieces of e4m3
+                            uint4 o;
+                            nibbles_to_e4m3(c.x, nib[j], o.x, o.y);
+                            nibbles_to_e4m3(c.y, nib[j], o.z, o.w);
+                            *reinterpret_cast<uint4 *>(arow + (((2 * piece) ^ (row & 7)) << 4)) = o;
+                            nibbles_to_e4m3(c.z, nib[j], o.x, o.y);
+                            nibbles_to_e4m3(c.w, nib[j], o.z, o.w);
+                            *reinterpret_cast<uint4 *>(arow + (((2 * piece + 1) ^ (row & 7)) << 4)) = o;
+                        } else {
+                            // 32 codes: four 16-byte pieces of bf16
+                            const uint32_t words[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                             for (int jj = 0; jj < 4; ++jj) {
                                 uint4 o;
-                                o.x = dequant_pair_mul(words[jj], mulz, negz);
-                                o.y = dequant_pair_mul(words[jj] >> 4, mulz, negz);
-                                o.z = dequant_pair_mul(words[jj] >> 8, mulz, negz);
-                                o.w = dequant_pair_mul(words[jj] >> 12, mulz, negz);
-                                *reinterpret_cast<uint4 *>(arow + (((4 * h + jj) ^ (i & 7)) << 4)) = o;
+                                o.x = dequant_pair_mul(words[jj], nib[j], negz[j]);
+                                o.y = dequant_pair_mul(words[jj] >> 4, nib[j], negz[j]);
+                                o.z = dequant_pair_mul(words[jj] >> 8, nib[j], negz[j]);
+                                o.w = dequant_pair_mul(words[jj] >> 12, nib[j], negz[j]);
+                                *reinterpret_cast<uint4 *>(arow + (((4 * piece + jj) ^ (row & 7)) << 4)) = o;
                             }
                         }
                     }
                     fence_proxy_async_smem();
                 }
-                __syncwarp();
-                if (lane == 0)
+                fetch(fu, fst, ahead[b]);
+                next(fu, fst, 2);
+                // the stage's copies have landed too: ready for the MMAs
+                ok = ok && warp_wait(full0 + 8 * slot, phase, &abort_flag, p.status);
+                if (lane == 0 && ok)
                     mbar_arrive_remote(ready0 + 8 * slot, 0);
+                next(u, st, 2);
+                slot += 2;
+                if (slot >= S) {
+                    slot -= S;
+                    phase ^= 1;
+                }
             }
         }
     }
@@ -490,13 +597,12 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     }
 }
 
-using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
-                        PairParams);
+using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PairParams);
 
 }  // namespace
 
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
-                           const CUtensorMap &codes, const CUtensorMap &bt, int *status, cudaStream_t st, int num_sms,
+                           const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,
                            unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
                            const float2 *rowc)
 {
@@ -537,6 +643,8 @@ cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, 
     p.rp = pk.rp;
     p.n_ttiles = (int)((M + BN - 1) / BN);
     p.n_units = p.n_ttiles * (int)((pk.Np + 2 * BM - 1) / (2 * BM));
+    p.stages = pair_stages(epi.mul != nullptr);
+    p.codes = reinterpret_cast<const uint8_t *>(pk.codes);
     p.s = pk.s;
     p.z = pk.z;
     p.status = status;
@@ -545,7 +653,7 @@ cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, 
     p.epi = epi;
     p.rowc = rowc;
     const PairFn fn = form == kQ8 ? tc_pair_kernel<kQ8> : tc_pair_kernel<kEpi>;
-    const int smem = pair_smem_bytes(form);
+    const int smem = pair_smem_bytes(epi.mul != nullptr);
     e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
     if (e != cudaSuccess)
         return e;
@@ -559,7 +667,7 @@ cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, tm_x, codes, use_ec ? bt : codes, tm_v, tm_mul, tm_res, tm_y, p);
+    return cudaLaunchKernelEx(&cfg, fn, tm_x, use_ec ? *bt : tm_x, tm_v, tm_mul, tm_res, tm_y, p);
 }
 
 }  // namespace spear
