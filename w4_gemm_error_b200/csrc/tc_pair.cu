@@ -187,8 +187,8 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     constexpr int SUB = 256 / BK;
     constexpr int GROUP_WARPS = 4;
     extern __shared__ uint8_t smem_raw[];
-    // full, ready and empty of each stage; accumulator full and empty; slot full and empty; drain
-    __shared__ __align__(8) uint64_t bars[3 * MAX_STAGES + 4 + 2 * NSLOT + 1];
+    // ready and empty of each stage; accumulator full and empty; slot full and empty; drain
+    __shared__ __align__(8) uint64_t bars[2 * MAX_STAGES + 4 + 2 * NSLOT + 1];
     __shared__ uint32_t tmem_base_slot;
     __shared__ volatile int abort_flag;
 
@@ -196,14 +196,15 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t *const base_ptr = smem_raw + (base - smem_addr(smem_raw));
     const uint32_t rank = cluster_ctarank();
-    const uint32_t full0 = smem_addr(&bars[0]);
-    const uint32_t ready0 = smem_addr(&bars[MAX_STAGES]);         // first CTA's: both CTAs' operands are staged
-    const uint32_t empty0 = smem_addr(&bars[2 * MAX_STAGES]);
-    const uint32_t tfull0 = smem_addr(&bars[3 * MAX_STAGES]);
-    const uint32_t tempty0 = smem_addr(&bars[3 * MAX_STAGES + 2]);   // first CTA's: both epilogues are done
-    const uint32_t sfull0 = smem_addr(&bars[3 * MAX_STAGES + 4]);
-    const uint32_t sempty0 = smem_addr(&bars[3 * MAX_STAGES + 4 + NSLOT]);
-    const uint32_t drain = smem_addr(&bars[3 * MAX_STAGES + 4 + 2 * NSLOT]);
+    // first CTA's: both CTAs' operands of the stage are there (the copies of both
+    // count their bytes on it, the dequantising warps of both arrive on it)
+    const uint32_t ready0 = smem_addr(&bars[0]);
+    const uint32_t empty0 = smem_addr(&bars[MAX_STAGES]);
+    const uint32_t tfull0 = smem_addr(&bars[2 * MAX_STAGES]);
+    const uint32_t tempty0 = smem_addr(&bars[2 * MAX_STAGES + 2]);   // first CTA's: both epilogues are done
+    const uint32_t sfull0 = smem_addr(&bars[2 * MAX_STAGES + 4]);
+    const uint32_t sempty0 = smem_addr(&bars[2 * MAX_STAGES + 4 + NSLOT]);
+    const uint32_t drain = smem_addr(&bars[2 * MAX_STAGES + 4 + 2 * NSLOT]);
     const uint32_t S = (uint32_t)p.stages;
     const bool has_mul = p.epi.mul != nullptr, has_res = p.epi.residual != nullptr;
     // byte offsets: residual / y halves of the slots, multiplier halves, per-token constants
@@ -213,8 +214,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     if (tid == 0) {
         abort_flag = 0;
         for (uint32_t s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, 1);
-            mbar_init(ready0 + 8 * s, 2 * GROUP_WARPS);
+            mbar_init(ready0 + 8 * s, 2 * GROUP_WARPS + 1);
             mbar_init(empty0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -251,6 +251,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (!p.v_ready)
             pdl_wait();   // x and v come from earlier kernels in the stream
         bool v_seen = p.v_ready == nullptr;
+        const uint32_t lead0 = map_to_rank(ready0, 0);
         uint32_t slot = 0, phase = 0, issued = 0;
         bool ok = true;
         for (int u = cluster; u < p.n_units && ok; u += n_clusters) {
@@ -261,11 +262,12 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     ok = false;
                     break;
                 }
-                const uint32_t sb = base + slot * STAGE_BYTES, full = full0 + 8 * slot;
+                const uint32_t sb = base + slot * STAGE_BYTES, ready = lead0 + 8 * slot;
                 if (i < p.n_main) {
                     if (elected) {
-                        mbar_expect_tx(full, B_BYTES);
-                        tma_load_2d(sb + A_BYTES, &tm_x, i * BK, t0, full);
+                        if (rank == 0)
+                            mbar_expect_tx(ready0 + 8 * slot, 2 * B_BYTES);
+                        tma_load_2d_pair(sb + A_BYTES, &tm_x, i * BK, t0, ready);
                     }
                 } else {
                     if (!v_seen && !__all_sync(0xffffffffu, wait_prepass(p, &abort_flag))) {
@@ -275,9 +277,10 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     v_seen = true;
                     if (elected) {
                         const int e = i - p.n_main;   // 32 tf32 values of j a stage
-                        mbar_expect_tx(full, A_BYTES + B_BYTES);
-                        tma_load_2d(sb, &tm_bt, e * 32, n0, full);
-                        tma_load_2d(sb + A_BYTES, &tm_v, e * 32, t0, full);
+                        if (rank == 0)
+                            mbar_expect_tx(ready0 + 8 * slot, 2 * (A_BYTES + B_BYTES));
+                        tma_load_2d_pair(sb, &tm_bt, e * 32, n0, ready);
+                        tma_load_2d_pair(sb + A_BYTES, &tm_v, e * 32, t0, ready);
                     }
                 }
                 ++issued;
@@ -287,12 +290,13 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 }
             }
         }
-        // do not leave while copies this CTA issued may still land (the
-        // dequantisers waited for every stage unless a wait gave up)
-        if (abort_flag)
+        // the pair does not leave while copies may still land (the MMA issuer
+        // waited for every stage of both CTAs unless a wait gave up; the second
+        // CTA waits for the first in the cluster barrier at the end)
+        if (abort_flag && rank == 0)
             for (uint32_t k = 0; k < S && k < issued; ++k) {
                 const uint32_t g = issued - 1 - k;
-                mbar_wait_final(full0 + 8 * (g % S), (g / S) & 1);
+                mbar_wait_final(ready0 + 8 * (g % S), (g / S) & 1);
             }
         // early start: this grid completes only after its predecessor
         if (p.v_ready)
@@ -479,34 +483,41 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         constexpr int kRowStep = 32 / Piece::kLanes;   // rows between a thread's pieces
         const int grp = (warp - DEQ_WARP) / GROUP_WARPS, w = warp & 3;
         const int piece = lane % Piece::kLanes, r0 = 32 * w + lane / Piece::kLanes;
-        // stages of this group in order: (unit, stage) pairs two stages apart
-        auto next = [&](int &u, int &st, int by) {
-            st += by;
-            while (st >= nst && u < p.n_units) {
-                st -= nst;
-                u += n_clusters;
-            }
+        // this group's stages in order, two apart: (u, st) the one at work, (fu, fst)
+        // the one whose codes are fetched, `src` its unit's codes (null: none)
+        const int64_t thread_off = (int64_t)(r0 & 63) * 128 + piece * 16;
+        int u = cluster, st = grp, fu = cluster, fst = grp;
+        const uint8_t *src = nullptr;
+        auto enter = [&]() {   // the fetching side's unit is fu
+            const int nb = (fu / p.n_ttiles) * 4 + (int)rank * 2 + (w >> 1);   // 64-row block of this warp's rows
+            src = fu < p.n_units && (int64_t)nb * 64 < p.Np
+                      ? p.codes + (int64_t)nb * p.kchunks * 8192 + thread_off : nullptr;
         };
-        // the codes do not depend on earlier kernels (no wait)
-        auto fetch = [&](int u, int st, Piece &c) {
-            const int nb = (u / p.n_ttiles) * 4 + (int)rank * 2 + (w >> 1);   // 64-row block of this warp's rows
-            const bool some = u < p.n_units && st < p.n_main && (int64_t)nb * 64 < p.Np;
-            const uint8_t *src = p.codes + (((int64_t)nb * p.kchunks + st / SUB) * 64 + (r0 & 63)) * 128 +
-                                 (st % SUB) * (BK / 2) + piece * 16;
+        auto fetch = [&](Piece &c) {   // (the codes do not depend on earlier kernels: no wait)
+            const bool some = src && fst < p.n_main;
+            const uint8_t *at = src + (int64_t)(fst / SUB) * 8192 + (fst % SUB) * (BK / 2);
 #pragma unroll
             for (int j = 0; j < Piece::kPieces; ++j)
-                c.w[j] = some ? ld_stream(src + j * kRowStep * 128) : make_uint4(0u, 0u, 0u, 0u);
+                c.w[j] = some ? ld_stream(at + j * kRowStep * 128) : make_uint4(0u, 0u, 0u, 0u);
+            fst += 2;
+            if (fst >= nst) {
+                while (fst >= nst && fu < p.n_units) {
+                    fst -= nst;
+                    fu += n_clusters;
+                }
+                enter();
+            }
         };
-        int u = cluster, st = 0, fu, fst;
-        next(u, st, grp);
+        while (st >= nst && u < p.n_units) {
+            st -= nst;
+            u += n_clusters;
+        }
         fu = u;
         fst = st;
+        enter();
         Piece ahead[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            fetch(fu, fst, ahead[b]);
-            next(fu, fst, 2);
-        }
+        fetch(ahead[0]);
+        fetch(ahead[1]);
         uint32_t slot = (uint32_t)grp, phase = 0;   // (at least two stages)
         int unit = -1;
         uint32_t nib[Piece::kPieces], negz[Piece::kPieces];   // kEpi: multiplier and bias of a row's pairs
@@ -532,6 +543,30 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         }
                     }
                 }
+                // dequantise before the stage is free: 32 codes a piece, two (e4m3) or
+                // four (bf16) 16-byte pieces of the operand
+                constexpr int kOut = FORM == kQ8 ? 2 : 4;
+                uint4 o[Piece::kPieces][kOut];
+#pragma unroll
+                for (int j = 0; j < Piece::kPieces; ++j) {
+                    const uint32_t words[4] = {ahead[b].w[j].x, ahead[b].w[j].y, ahead[b].w[j].z, ahead[b].w[j].w};
+                    if constexpr (FORM == kQ8) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            nibbles_to_e4m3(words[2 * h], nib[j], o[j][h].x, o[j][h].y);
+                            nibbles_to_e4m3(words[2 * h + 1], nib[j], o[j][h].z, o[j][h].w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            o[j][h].x = dequant_pair_mul(words[h], nib[j], negz[j]);
+                            o[j][h].y = dequant_pair_mul(words[h] >> 4, nib[j], negz[j]);
+                            o[j][h].z = dequant_pair_mul(words[h] >> 8, nib[j], negz[j]);
+                            o[j][h].w = dequant_pair_mul(words[h] >> 12, nib[j], negz[j]);
+                        }
+                    }
+                }
+                fetch(ahead[b]);
                 // the stage is free once the MMAs of its last round are done
                 ok = warp_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status);
                 if (ok && st < p.n_main) {
@@ -539,40 +574,21 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < Piece::kPieces; ++j) {
                         const int row = r0 + j * kRowStep;
-                        uint8_t *arow = at + row * ROW_BYTES;
-                        const uint4 c = ahead[b].w[j];
-                        if constexpr (FORM == kQ8) {
-                            // 32 codes: two 16-byte pieces of e4m3
-                            uint4 o;
-                            nibbles_to_e4m3(c.x, nib[j], o.x, o.y);
-                            nibbles_to_e4m3(c.y, nib[j], o.z, o.w);
-                            *reinterpret_cast<uint4 *>(arow + (((2 * piece) ^ (row & 7)) << 4)) = o;
-                            nibbles_to_e4m3(c.z, nib[j], o.x, o.y);
-                            nibbles_to_e4m3(c.w, nib[j], o.z, o.w);
-                            *reinterpret_cast<uint4 *>(arow + (((2 * piece + 1) ^ (row & 7)) << 4)) = o;
-                        } else {
-                            // 32 codes: four 16-byte pieces of bf16
-                            const uint32_t words[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                            for (int jj = 0; jj < 4; ++jj) {
-                                uint4 o;
-                                o.x = dequant_pair_mul(words[jj], nib[j], negz[j]);
-                                o.y = dequant_pair_mul(words[jj] >> 4, nib[j], negz[j]);
-                                o.z = dequant_pair_mul(words[jj] >> 8, nib[j], negz[j]);
-                                o.w = dequant_pair_mul(words[jj] >> 12, nib[j], negz[j]);
-                                *reinterpret_cast<uint4 *>(arow + (((4 * piece + jj) ^ (row & 7)) << 4)) = o;
-                            }
-                        }
+                        for (int h = 0; h < kOut; ++h)
+                            *reinterpret_cast<uint4 *>(at + row * ROW_BYTES + (((kOut * piece + h) ^ (row & 7)) << 4)) =
+                                o[j][h];
                     }
                     fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                fetch(fu, fst, ahead[b]);
-                next(fu, fst, 2);
-                // the stage's copies have landed too: ready for the MMAs
-                ok = ok && warp_wait(full0 + 8 * slot, phase, &abort_flag, p.status);
                 if (lane == 0 && ok)
                     mbar_arrive_remote(ready0 + 8 * slot, 0);
-                next(u, st, 2);
+                st += 2;
+                while (st >= nst && u < p.n_units) {
+                    st -= nst;
+                    u += n_clusters;
+                }
                 slot += 2;
                 if (slot >= S) {
                     slot -= S;
