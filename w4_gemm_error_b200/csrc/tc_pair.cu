@@ -14,7 +14,7 @@
 // tokens, and the MMAs read both halves of the activations from the two SMs,
 // so each SM stages half the activations for the same products.
 //
-// Roles in each CTA (20 warps):
+// Roles in each CTA (28 warps):
 //   warp 0       TMA producer of the stages: its 128 tokens of x (EC stages: v
 //                and B^T/e)
 //   warp 1       TMEM allocation; in the pair's first CTA the issuer of the
@@ -25,9 +25,9 @@
 //                lanes) taking alternate slots: accumulator from TMEM, the
 //                formula above, y into the slot (over the residual, element by
 //                element) and from there to HBM by one TMA store a slot
-//   warps 12-19  dequantisers, two groups of four taking alternate stages:
-//                codes from global memory into registers two stages of the
-//                group ahead, from there into the stage as MMA operands
+//   warps 12-27  dequantisers, four groups of four taking every fourth stage:
+//                codes from global memory into registers four stages ahead,
+//                from there into the stage as MMA operands
 // The codes never pass through shared memory before they are dequantised, so
 // that the ring of stages (5, or 6 without a multiplier) is deep enough to
 // cover the latency from a TMA request to the MMA that frees its stage: with
@@ -60,8 +60,8 @@ constexpr int CHUNK = 32;               // tokens of an epilogue slot
 constexpr int NSLOT = 4;
 constexpr int HALF_SLOT = CHUNK * BM * 2;   // residual / y; a second one for the multiplier
 constexpr int ROWC_BYTES = CHUNK * 8;
-constexpr int THREADS = 640;
-constexpr int EPI_WARP = 4, DEQ_WARP = 12;
+constexpr int EPI_WARP = 4, DEQ_WARP = 12, GROUP_WARPS = 4, GROUPS = 4;
+constexpr int THREADS = 32 * (DEQ_WARP + GROUPS * GROUP_WARPS);
 
 __host__ __device__ constexpr int pair_bk(int form) { return form == kQ8 ? 128 : 64; }
 // Ring depth and shared memory with and without a multiplier in the slots.
@@ -111,15 +111,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 // One slot's outputs of this thread: channel n (row `row` of the CTA), the 32
-// tokens of the chunk, the accumulator in acc.  mul and y are its columns of
+// tokens of the chunk, the accumulator at tacc in TMEM.  mul and y are its columns of
 // [32 tokens][128 channels] bf16.  Eight tokens at a time: every shared-memory
 // read of a group comes before its first store.
 template <int FORM, int ACT, bool MUL, bool RES>
-__device__ __forceinline__ void emit_chunk(const uint32_t (&acc)[CHUNK], float e_n, float z_n, float bias,
+__device__ __forceinline__ void emit_chunk(uint32_t tacc, float e_n, float z_n, float bias,
                                            const uint16_t *mul, uint16_t *y, const float4 *rc)
 {
 #pragma unroll
     for (int j0 = 0; j0 < CHUNK; j0 += 8) {
+        uint32_t acc[8];
+        tmem_ld_32x32b_x8(tacc + j0, acc);
         float v[8], m[8], r[8];
         float4 c[4];
 #pragma unroll
@@ -131,7 +133,7 @@ __device__ __forceinline__ void emit_chunk(const uint32_t (&acc)[CHUNK], float e
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            v[j] = __uint_as_float(acc[j0 + j]);
+            v[j] = __uint_as_float(acc[j]);
             if constexpr (FORM == kQ8) {
                 const float cx = (j & 1) ? c[j / 2].z : c[j / 2].x, cy = (j & 1) ? c[j / 2].w : c[j / 2].y;
                 v[j] = e_n * cx * (v[j] - z_n * cy);
@@ -154,16 +156,16 @@ __device__ __forceinline__ void emit_chunk(const uint32_t (&acc)[CHUNK], float e
 }
 
 template <int FORM, int ACT>
-__device__ __forceinline__ void emit_chunk_of(const uint32_t (&acc)[CHUNK], float e_n, float z_n, float bias,
+__device__ __forceinline__ void emit_chunk_of(uint32_t tacc, float e_n, float z_n, float bias,
                                               const uint16_t *mul, uint16_t *y, const float4 *rc, bool has_mul,
                                               bool has_res)
 {
     if (has_mul)
-        has_res ? emit_chunk<FORM, ACT, true, true>(acc, e_n, z_n, bias, mul, y, rc)
-                : emit_chunk<FORM, ACT, true, false>(acc, e_n, z_n, bias, mul, y, rc);
+        has_res ? emit_chunk<FORM, ACT, true, true>(tacc, e_n, z_n, bias, mul, y, rc)
+                : emit_chunk<FORM, ACT, true, false>(tacc, e_n, z_n, bias, mul, y, rc);
     else
-        has_res ? emit_chunk<FORM, ACT, false, true>(acc, e_n, z_n, bias, mul, y, rc)
-                : emit_chunk<FORM, ACT, false, false>(acc, e_n, z_n, bias, mul, y, rc);
+        has_res ? emit_chunk<FORM, ACT, false, true>(tacc, e_n, z_n, bias, mul, y, rc)
+                : emit_chunk<FORM, ACT, false, false>(tacc, e_n, z_n, bias, mul, y, rc);
 }
 
 // A dequantiser thread's codes of one stage: `kPieces` 16-byte pieces, lanes
@@ -185,7 +187,6 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 {
     constexpr int BK = pair_bk(FORM);
     constexpr int SUB = 256 / BK;
-    constexpr int GROUP_WARPS = 4;
     extern __shared__ uint8_t smem_raw[];
     // ready and empty of each stage; accumulator full and empty; slot full and empty; drain
     __shared__ __align__(8) uint64_t bars[2 * MAX_STAGES + 4 + 2 * NSLOT + 1];
@@ -408,6 +409,29 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 for (uint32_t k = 0; k < NSLOT && k < g; ++k)
                     mbar_wait_final(sfull0 + 8 * ((g - 1 - k) % NSLOT), ((g - 1 - k) / NSLOT) & 1);
         }
+    } else if (warp == 3) {
+        // ------------------------------------------------ codes from HBM to L2, one unit ahead.  The clusters
+        // that share a row of tiles read its codes at about the same time, so without this all of
+        // them wait for HBM; the cluster that has the row's first token tile asks for all
+        if (lane == 0) {
+            const uint32_t row_bytes = (uint32_t)p.kchunks * 8192u;   // codes of 64 rows
+            auto prefetch = [&](int u) {
+                if (u >= p.n_units || (u % p.n_ttiles != 0 && u >= n_clusters))
+                    return;
+                const int64_t nb = (int64_t)(u / p.n_ttiles) * 4 + (int)rank * 2;
+                if (nb * 64 >= p.Np)
+                    return;
+                for (uint32_t at = 0; at < 2 * row_bytes; at += 16384)   // (Np is a multiple of 128)
+                    bulk_prefetch_l2(p.codes + nb * row_bytes + at, 16384);
+            };
+            prefetch(cluster);
+            int lt = 0;
+            for (int u = cluster; u < p.n_units; u += n_clusters, ++lt) {
+                prefetch(u + n_clusters);
+                if (!mbar_wait(tfull0 + 8 * (lt & 1), (lt >> 1) & 1, &abort_flag, p.status))
+                    break;
+            }
+        }
     } else if (warp >= EPI_WARP && warp < DEQ_WARP) {
         // ------------------------------------------------ epilogue: set `set` takes slots g with g % 2 == set,
         // warp quarter q owns TMEM lanes 32q .. 32q + 31 (channels)
@@ -436,8 +460,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 const uint32_t slot = g % NSLOT;
                 ok = ok && mbar_wait(sfull0 + 8 * slot, (g / NSLOT) & 1, &abort_flag, p.status);
                 __syncwarp();
-                uint32_t acc[CHUNK];
-                tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(32 * q) << 16) + buf * BN + CHUNK * c, acc);
+                const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16) + buf * BN + CHUNK * c;
                 const uint16_t *mul = reinterpret_cast<const uint16_t *>(base_ptr + o_mul + slot * HALF_SLOT) + row;
                 uint16_t *y = reinterpret_cast<uint16_t *>(base_ptr + o_y + slot * HALF_SLOT) + row;
                 const float4 *rc = reinterpret_cast<const float4 *>(base_ptr + o_rowc + slot * ROWC_BYTES);
@@ -478,15 +501,15 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (storer)
             bulk_wait_all();   // the stores are complete (and the slots read) before the CTA leaves
     } else if (warp >= DEQ_WARP) {
-        // ------------------------------------------------ dequantisers: group `grp` takes every second stage
+        // ------------------------------------------------ dequantisers: group `grp` takes every fourth stage
         using Piece = Codes<FORM>;
         constexpr int kRowStep = 32 / Piece::kLanes;   // rows between a thread's pieces
         const int grp = (warp - DEQ_WARP) / GROUP_WARPS, w = warp & 3;
         const int piece = lane % Piece::kLanes, r0 = 32 * w + lane / Piece::kLanes;
-        // this group's stages in order, two apart: (u, st) the one at work, (fu, fst)
+        // this group's stages in order, GROUPS apart: (u, st) the one at work, (fu, fst)
         // the one whose codes are fetched, `src` its unit's codes (null: none)
         const int64_t thread_off = (int64_t)(r0 & 63) * 128 + piece * 16;
-        int u = cluster, st = grp, fu = cluster, fst = grp;
+        int u = cluster, st = grp, fu = 0, fst = 0;
         const uint8_t *src = nullptr;
         auto enter = [&]() {   // the fetching side's unit is fu
             const int nb = (fu / p.n_ttiles) * 4 + (int)rank * 2 + (w >> 1);   // 64-row block of this warp's rows
@@ -499,7 +522,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 #pragma unroll
             for (int j = 0; j < Piece::kPieces; ++j)
                 c.w[j] = some ? ld_stream(at + j * kRowStep * 128) : make_uint4(0u, 0u, 0u, 0u);
-            fst += 2;
+            fst += GROUPS;
             if (fst >= nst) {
                 while (fst >= nst && fu < p.n_units) {
                     fst -= nst;
@@ -515,85 +538,79 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         fu = u;
         fst = st;
         enter();
-        Piece ahead[2];
-        fetch(ahead[0]);
-        fetch(ahead[1]);
-        uint32_t slot = (uint32_t)grp, phase = 0;   // (at least two stages)
+        Piece ahead;
+        fetch(ahead);
+        uint32_t slot = (uint32_t)grp, phase = 0;   // (the ring has more stages than there are groups)
         int unit = -1;
         uint32_t nib[Piece::kPieces], negz[Piece::kPieces];   // kEpi: multiplier and bias of a row's pairs
         bool ok = true;
         while (u < p.n_units && ok) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (u >= p.n_units || !ok)
-                    break;
-                if (unit != u) {
-                    unit = u;
-                    const int64_t n0 = (int64_t)(u / p.n_ttiles) * 2 * BM + rank * BM + r0;
-#pragma unroll
-                    for (int j = 0; j < Piece::kPieces; ++j) {
-                        // a row whose s is 0 has weights 0, whatever its codes (the epilogue scales it by 1)
-                        const int64_t n = n0 + j * kRowStep;
-                        const bool live = n < p.Np && __ldg(p.s + n) != 0.0f;
-                        if constexpr (FORM == kQ8) {
-                            nib[j] = live ? 0x0F0F0F0Fu : 0u;
-                        } else {
-                            nib[j] = live ? 0x3F803F80u : 0u;
-                            negz[j] = live ? dequant_bias<false>(__ldg(p.z + n)) : 0u;
-                        }
-                    }
-                }
-                // dequantise before the stage is free: 32 codes a piece, two (e4m3) or
-                // four (bf16) 16-byte pieces of the operand
-                constexpr int kOut = FORM == kQ8 ? 2 : 4;
-                uint4 o[Piece::kPieces][kOut];
+            if (unit != u) {
+                unit = u;
+                const int64_t n0 = (int64_t)(u / p.n_ttiles) * 2 * BM + rank * BM + r0;
 #pragma unroll
                 for (int j = 0; j < Piece::kPieces; ++j) {
-                    const uint32_t words[4] = {ahead[b].w[j].x, ahead[b].w[j].y, ahead[b].w[j].z, ahead[b].w[j].w};
+                    // a row whose s is 0 has weights 0, whatever its codes (the epilogue scales it by 1)
+                    const int64_t n = n0 + j * kRowStep;
+                    const bool live = n < p.Np && __ldg(p.s + n) != 0.0f;
                     if constexpr (FORM == kQ8) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            nibbles_to_e4m3(words[2 * h], nib[j], o[j][h].x, o[j][h].y);
-                            nibbles_to_e4m3(words[2 * h + 1], nib[j], o[j][h].z, o[j][h].w);
-                        }
+                        nib[j] = live ? 0x0F0F0F0Fu : 0u;
                     } else {
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            o[j][h].x = dequant_pair_mul(words[h], nib[j], negz[j]);
-                            o[j][h].y = dequant_pair_mul(words[h] >> 4, nib[j], negz[j]);
-                            o[j][h].z = dequant_pair_mul(words[h] >> 8, nib[j], negz[j]);
-                            o[j][h].w = dequant_pair_mul(words[h] >> 12, nib[j], negz[j]);
-                        }
+                        nib[j] = live ? 0x3F803F80u : 0u;
+                        negz[j] = live ? dequant_bias<false>(__ldg(p.z + n)) : 0u;
                     }
                 }
-                fetch(ahead[b]);
-                // the stage is free once the MMAs of its last round are done
-                ok = warp_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status);
-                if (ok && st < p.n_main) {
-                    uint8_t *const at = base_ptr + slot * STAGE_BYTES;
+            }
+            // dequantise before the stage is free: 32 codes a piece, two (e4m3) or
+            // four (bf16) 16-byte pieces of the operand
+            constexpr int kOut = FORM == kQ8 ? 2 : 4;
+            uint4 o[Piece::kPieces][kOut];
 #pragma unroll
-                    for (int j = 0; j < Piece::kPieces; ++j) {
-                        const int row = r0 + j * kRowStep;
+            for (int j = 0; j < Piece::kPieces; ++j) {
+                const uint32_t words[4] = {ahead.w[j].x, ahead.w[j].y, ahead.w[j].z, ahead.w[j].w};
+                if constexpr (FORM == kQ8) {
 #pragma unroll
-                        for (int h = 0; h < kOut; ++h)
-                            *reinterpret_cast<uint4 *>(at + row * ROW_BYTES + (((kOut * piece + h) ^ (row & 7)) << 4)) =
-                                o[j][h];
+                    for (int h = 0; h < 2; ++h) {
+                        nibbles_to_e4m3(words[2 * h], nib[j], o[j][h].x, o[j][h].y);
+                        nibbles_to_e4m3(words[2 * h + 1], nib[j], o[j][h].z, o[j][h].w);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        o[j][h].x = dequant_pair_mul(words[h], nib[j], negz[j]);
+                        o[j][h].y = dequant_pair_mul(words[h] >> 4, nib[j], negz[j]);
+                        o[j][h].z = dequant_pair_mul(words[h] >> 8, nib[j], negz[j]);
+                        o[j][h].w = dequant_pair_mul(words[h] >> 12, nib[j], negz[j]);
+                    }
                 }
-                if (lane == 0 && ok)
-                    mbar_arrive_remote(ready0 + 8 * slot, 0);
-                st += 2;
-                while (st >= nst && u < p.n_units) {
-                    st -= nst;
-                    u += n_clusters;
+            }
+            fetch(ahead);
+            // the stage is free once the MMAs of its last round are done
+            ok = warp_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status);
+            if (ok && st < p.n_main) {
+                uint8_t *const at = base_ptr + slot * STAGE_BYTES;
+#pragma unroll
+                for (int j = 0; j < Piece::kPieces; ++j) {
+                    const int row = r0 + j * kRowStep;
+#pragma unroll
+                    for (int h = 0; h < kOut; ++h)
+                        *reinterpret_cast<uint4 *>(at + row * ROW_BYTES + (((kOut * piece + h) ^ (row & 7)) << 4)) =
+                            o[j][h];
                 }
-                slot += 2;
-                if (slot >= S) {
-                    slot -= S;
-                    phase ^= 1;
-                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0 && ok)
+                mbar_arrive_remote(ready0 + 8 * slot, 0);
+            st += GROUPS;
+            while (st >= nst && u < p.n_units) {
+                st -= nst;
+                u += n_clusters;
+            }
+            slot += GROUPS;
+            if (slot >= S) {
+                slot -= S;
+                phase ^= 1;
             }
         }
     }
