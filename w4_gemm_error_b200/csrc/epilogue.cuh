@@ -25,10 +25,27 @@ struct Epilogue {
     const float *xs = nullptr;            // [M] scale of each token's e4m3 activations (kQ8)
 };
 
-// v / (1 + exp(-c)).  The fast exponential and reciprocal are off by a few
-// units of 2^-23 |c| at most, far inside the bf16 rounding of the result; a
-// large negative c gives exp = inf and a result of zero.
-__device__ __forceinline__ float times_sigmoid(float v, float c) { return __fdividef(v, 1.0f + __expf(-c)); }
+// 1 / (1 + exp(-c)), by the hardware's exp2 and reciprocal.  They are off by a
+// few units of 2^-23 |c| at most, far inside the bf16 rounding of the result; a
+// large negative c gives exp = inf and a sigmoid of zero.
+__device__ __forceinline__ float ex2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGeluK = 1.5957691216057308f, kGeluK3 = 0.071354816272600f;   // 2 sqrt(2/pi), and times 0.044715
+__device__ __forceinline__ float times_sigmoid(float v, float c)
+{
+    return v * rcp_approx(1.0f + ex2_approx(-kLog2e * c));
+}
 
 __device__ __forceinline__ float activate(float v, int act)
 {
@@ -38,8 +55,61 @@ __device__ __forceinline__ float activate(float v, int act)
     // v Phi(v), by erfc so that the negative tail keeps its relative accuracy
     case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
     // 0.5 (1 + tanh a) = 1 / (1 + exp(-2a)), a = sqrt(2/pi) (v + 0.044715 v^3)
-    case kActGeluTanh: return times_sigmoid(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));
+    case kActGeluTanh: return times_sigmoid(v, v * fmaf(kGeluK3, v * v, kGeluK));
     default: return v;
+    }
+}
+
+// Two fp32 values in one register pair, and the packed fp32 instructions of
+// sm_100 on them (each half rounded as the scalar instruction rounds it).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 f2_pack(float lo, float hi)
+{
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void f2_unpack(f32x2 v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// activate() of two values.
+template <int ACT>
+__device__ __forceinline__ f32x2 activate2(f32x2 v)
+{
+    if constexpr (ACT == kActNone) {
+        return v;
+    } else if constexpr (ACT == kActSilu || ACT == kActGeluTanh) {
+        f32x2 c = v;
+        if constexpr (ACT == kActGeluTanh)
+            c = f2_mul(v, f2_fma(f2_pack(kGeluK3, kGeluK3), f2_mul(v, v), f2_pack(kGeluK, kGeluK)));
+        float a, b;
+        f2_unpack(f2_mul(c, f2_pack(-kLog2e, -kLog2e)), a, b);
+        f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), f2_pack(1.f, 1.f)), a, b);
+        return f2_mul(v, f2_pack(rcp_approx(a), rcp_approx(b)));
+    } else {
+        float a, b;
+        f2_unpack(v, a, b);
+        return f2_pack(activate(a, ACT), activate(b, ACT));
     }
 }
 

@@ -2,7 +2,7 @@
 // epilogue: the token's scale and code sum, and with the Error Compensator the
 // gated down-projection.
 //
-//   X_t = sum_k xq[t,k]                     rowc[t] = (2^9 xs[t], 2^-9 X_t)
+//   X_t = sum_k xq[t,k]                     rowc: 2^9 xs[t] and 2^-9 X_t
 //   u   = xq[t,:] . [w_g, A]                (of the codes; xs[t] times it is the layer's)
 //   g_t = 1 / (1 + exp(-(xs[t] u_0 + b_g)))
 //   v   = 2^-9 g_t u_j, rounded to tf32     [M][rp]
@@ -37,7 +37,7 @@ struct PrepassQ8Params {
     float b_g;
     int S, bps;             // splits of K, 64-k blocks a split
     float *v;
-    float2 *rowc;
+    float *rowc;
     float *part;            // [tiles][S][(R1p + 1) x 16]
     unsigned *counters;     // [tiles], zero between calls
     unsigned *ready;        // counted (release) once per token tile; null for none
@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(128) prepass_q8_kernel(PrepassQ8Params p)
     __shared__ float s_gate[kTok];
     if (tid < kTok && t0 + tid < p.M) {
         const float xs = __ldg(p.xs + t0 + tid);
-        p.rowc[t0 + tid] = make_float2(512.0f * xs, red[kRowsG * kTok + tid] * (1.0f / 512.0f));
+        p.rowc[rowc_at(t0 + tid)] = 512.0f * xs;
+        p.rowc[rowc_at(t0 + tid) + 2] = red[kRowsG * kTok + tid] * (1.0f / 512.0f);
         if (MT > 0)
             s_gate[tid] = 1.0f / (1.0f + expf(-(xs * red[tid] + p.b_g)));
     }
@@ -231,7 +232,7 @@ cudaError_t prepass_q8_alloc(const Packed &pk, int64_t max_M, int num_sms, Prepa
     w.part_floats = worst;
     w.n_counters = (int)tiles;
     // whole chunks of 32 tokens, zero where no token is (a copy of a chunk reads all of it)
-    const size_t rowc_bytes = (size_t)((max_M + 31) / 32 * 32) * sizeof(float2);
+    const size_t rowc_bytes = (size_t)((max_M + 31) / 32 * 32) * 2 * sizeof(float);
     cudaError_t e = cudaMalloc(&w.rowc, rowc_bytes);
     if (e == cudaSuccess)
         e = cudaMemset(w.rowc, 0, rowc_bytes);

@@ -99,7 +99,7 @@ struct TcParams {
     unsigned *v_ready;
     unsigned v_expected;
     Epilogue epi;          // forms kEpi and kQ8
-    const float2 *rowc;    // form kQ8: [M] (2^9 xs[t], 2^-9 sum_k xq[t,k]) from the prepass
+    const float *rowc;     // form kQ8: 2^9 xs[t] and 2^-9 sum_k xq[t,k] from the prepass (rowc_at)
 };
 
 struct Maps {
@@ -284,7 +284,8 @@ __device__ __forceinline__ void store_outputs8(const TcParams &p, int64_t t, int
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if constexpr (FORM == kQ8)
-                rc[j] = t + j < p.M ? __ldcg(p.rowc + t + j) : make_float2(0.f, 0.f);
+                rc[j] = t + j < p.M ? make_float2(__ldcg(p.rowc + rowc_at(t + j)), __ldcg(p.rowc + rowc_at(t + j) + 2))
+                                    : make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             eo[j].bias = bias;
@@ -783,7 +784,7 @@ TcFn tc_fn(int BN)
 cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                       const TcWork &w, int *status, bool zero_wait_budget, cudaStream_t st, int num_sms,
                       unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
-                      const float2 *rowc)
+                      const float *rowc)
 {
     if (M <= 0)
         return cudaSuccess;

@@ -17,12 +17,15 @@ struct TcWork {
 
 // Workspace of the 8-bit form's prepass.
 struct PrepassQ8Work {
-    float2 *rowc = nullptr;      // [max_M]
+    // two constants a token, pairs of tokens together: c0[2i], c0[2i+1], c1[2i],
+    // c1[2i+1] (rowc_at); max_M tokens rounded up to 32
+    float *rowc = nullptr;
     float *part = nullptr;       // split-K partials
     size_t part_floats = 0;
     unsigned *counters = nullptr;
     int n_counters = 0;
 };
+__host__ __device__ constexpr int64_t rowc_at(int64_t t) { return 4 * (t / 2) + (t & 1); }   // c0; c1 is 2 on
 cudaError_t prepass_q8_alloc(const Packed &pk, int64_t max_M, int num_sms, PrepassQ8Work &w);
 void prepass_q8_free(PrepassQ8Work &w);
 // rowc and (with `ec`) v of M tokens of e4m3 activations, rows ldx apart; see
@@ -52,7 +55,7 @@ cudaError_t launch_tc_prepass(const Packed &pk, const void *x, int64_t M, float 
 cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                       const TcWork &w, int *status, bool zero_wait_budget, cudaStream_t st, int num_sms,
                       unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
-                      const float2 *rowc);
+                      const float *rowc);
 
 // The forms kEpi and kQ8 from kPairMinTokens tokens on (tc_pair.cu; launch_tc
 // takes it).  bt: the tensor map of B^T/e; rowc holds whole chunks of 32 tokens.
@@ -60,6 +63,6 @@ constexpr int64_t kPairMinTokens = 129;
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                            const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,
                            unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
-                           const float2 *rowc);
+                           const float *rowc);
 
 }  // namespace spear

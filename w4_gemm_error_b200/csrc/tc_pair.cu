@@ -84,7 +84,7 @@ struct PairParams {
     unsigned *v_ready;       // as TcParams::v_ready (tc_gemm.cu)
     unsigned v_expected;
     Epilogue epi;
-    const float2 *rowc;      // form kQ8: as TcParams::rowc, padded to whole chunks
+    const float *rowc;       // form kQ8: as TcParams::rowc, padded to whole chunks
 };
 
 // Bounded wait until the prepass has counted everything it writes.
@@ -118,39 +118,42 @@ template <int FORM, int ACT, bool MUL, bool RES>
 __device__ __forceinline__ void emit_chunk(uint32_t tacc, float e_n, float z_n, float bias,
                                            const uint16_t *mul, uint16_t *y, const float4 *rc)
 {
+    const f32x2 e2 = f2_pack(e_n, e_n), nz2 = f2_pack(-z_n, -z_n), bias2 = f2_pack(bias, bias);
 #pragma unroll
     for (int j0 = 0; j0 < CHUNK; j0 += 8) {
         uint32_t acc[8];
         tmem_ld_32x32b_x8(tacc + j0, acc);
-        float v[8], m[8], r[8];
-        float4 c[4];
+        float4 c[4];   // per-token constants of two tokens: both first ones, both second ones
+        uint32_t m[8], r[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (FORM == kQ8 && (j & 1) == 0)
-                c[j / 2] = rc[(j0 + j) / 2];   // the constants of two tokens
-            m[j] = MUL ? bf16_lo(mul[(j0 + j) * BM]) : 1.f;
-            r[j] = RES ? bf16_lo(y[(j0 + j) * BM]) : 0.f;
+                c[j / 2] = rc[(j0 + j) / 2];
+            m[j] = MUL ? mul[(j0 + j) * BM] : 0u;
+            r[j] = RES ? y[(j0 + j) * BM] : 0u;
         }
+        uint32_t two[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = __uint_as_float(acc[j]);
+        for (int j = 0; j < 8; j += 2) {
+            f32x2 v = f2_pack(__uint_as_float(acc[j]), __uint_as_float(acc[j + 1]));
+            f32x2 k = e2;
             if constexpr (FORM == kQ8) {
-                const float cx = (j & 1) ? c[j / 2].z : c[j / 2].x, cy = (j & 1) ? c[j / 2].w : c[j / 2].y;
-                v[j] = e_n * cx * (v[j] - z_n * cy);
-            } else {
-                v[j] *= e_n;
+                k = f2_mul(e2, f2_pack(c[j / 2].x, c[j / 2].y));
+                v = f2_fma(nz2, f2_pack(c[j / 2].z, c[j / 2].w), v);
             }
-            v[j] = activate(v[j] + bias, ACT);
+            v = activate2<ACT>(f2_fma(k, v, bias2));
             if (MUL)
-                v[j] *= m[j];
+                v = f2_mul(v, f2_pack(bf16_lo(m[j]), bf16_lo(m[j + 1])));
             if (RES)
-                v[j] += r[j];
+                v = f2_add(v, f2_pack(bf16_lo(r[j]), bf16_lo(r[j + 1])));
+            float lo, hi;
+            f2_unpack(v, lo, hi);
+            two[j / 2] = pack_bf16x2(lo, hi);
         }
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            const uint32_t two = pack_bf16x2(v[j], v[j + 1]);
-            y[(j0 + j) * BM] = (uint16_t)two;
-            y[(j0 + j + 1) * BM] = (uint16_t)(two >> 16);
+            y[(j0 + j) * BM] = (uint16_t)two[j / 2];
+            y[(j0 + j + 1) * BM] = (uint16_t)(two[j / 2] >> 16);
         }
     }
 }
@@ -401,7 +404,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     if (has_res)
                         tma_load_2d(base + o_y + slot * HALF_SLOT, &tm_res, n0, t0 + c * CHUNK, bar);
                     if (FORM == kQ8)
-                        bulk_load(base + o_rowc + slot * ROWC_BYTES, p.rowc + t0 + c * CHUNK, ROWC_BYTES, bar);
+                        bulk_load(base + o_rowc + slot * ROWC_BYTES, p.rowc + 2 * (t0 + c * CHUNK), ROWC_BYTES, bar);
                 }
             }
             // (the epilogue waited for every slot unless a wait gave up)
@@ -637,7 +640,7 @@ using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUte
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                            const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,
                            unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
-                           const float2 *rowc)
+                           const float *rowc)
 {
     const int BK = pair_bk(form);
     const uint64_t xd[2] = {(uint64_t)pk.K, (uint64_t)M};
