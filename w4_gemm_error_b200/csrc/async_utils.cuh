@@ -420,6 +420,13 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
 // Counter increment that releases (cumulatively) every write this thread has
 // observed, including its CTA's writes ordered before it by a CTA barrier.
 __device__ __forceinline__ void red_release_gpu_add(unsigned *p, unsigned v)

@@ -172,8 +172,12 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
     const bool early = ec && fused && (choice & SPEAR_FORCE_TC) && tc_supported(h);
     unsigned expected = 0;
     if (ec && !(decode && fused)) {
-        e = run_prepass(h, x, M, (choice & SPEAR_FORCE_TC) != 0 && fused, st, early ? h->vready : nullptr,
-                        &expected);
+        if (form == kEpi && M >= kPairMinTokens)
+            e = launch_tc_prepass2(pk, x, pk.K, nullptr, M, true, h->v, nullptr, kEpi, tc_map_g(h->tc), h->status, st,
+                                   h->num_sms, early ? h->vready : nullptr, &expected);
+        else
+            e = run_prepass(h, x, M, (choice & SPEAR_FORCE_TC) != 0 && fused, st, early ? h->vready : nullptr,
+                            &expected);
         if (e != cudaSuccess)
             return from_cuda(e);
     }
@@ -264,12 +268,16 @@ int run_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y
         // as in run_forward: with the EC the product's main stages start beside
         // the prepass, which counts what it has written into vready
         unsigned expected = 0;
-        cudaError_t e = launch_prepass_q8(pk, xq, ldx, xs, M, ec, h->v, h->preq8, st, h->num_sms,
-                                          ec ? h->vready : nullptr, &expected);
+        unsigned *ready = ec ? h->vready : nullptr;
+        cudaError_t e = M >= kPairMinTokens
+                            ? launch_tc_prepass2(pk, xq, ldx, xs, M, ec, h->v, h->preq8.rowc, kQ8, tc_map_g(h->tc),
+                                                 h->status, st, h->num_sms, ready, &expected)
+                            : launch_prepass_q8(pk, xq, ldx, xs, M, ec, h->v, h->preq8, st, h->num_sms, ready,
+                                                &expected);
         if (e != cudaSuccess)
             return from_cuda(e);
         e = launch_tc(pk, xq, y, M, h->v, ec, h->tc, h->status, h->fault_timeout, st, h->num_sms,
-                      ec ? h->vready : nullptr, expected, kQ8, epi, ldx, h->preq8.rowc);
+                      ready, expected, kQ8, epi, ldx, h->preq8.rowc);
         if (e != cudaSuccess || (ec && h->fault_timeout))
             cudaMemsetAsync(h->vready, 0, 2 * sizeof(unsigned), st);
         return from_cuda(e);
@@ -528,6 +536,12 @@ int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M
     DeviceGuard guard(h->device);
     if (!guard.ok())
         return SPEAR_ERR_CUDA;
+    // nothing after the layer: the plain forward, its EC in the product's kernel
+    if (!epi.bias && !epi.mul && !epi.residual && epi.act == kActNone) {
+        if (flags & SPEAR_FORCE_SPLIT)
+            return SPEAR_ERR_UNSUPPORTED;
+        return run_forward(h, x, y, M, flags | SPEAR_FORCE_FUSED, static_cast<cudaStream_t>(stream));
+    }
     return run_forward(h, x, y, M, flags, static_cast<cudaStream_t>(stream), kEpi, epi);
 }
 

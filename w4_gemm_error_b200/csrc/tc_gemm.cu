@@ -695,6 +695,8 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 
 bool tc_available(const Packed &) { return tensor_maps_available(); }
 
+const CUtensorMap *tc_map_g(const TcWork &w) { return &static_cast<const Maps *>(w.maps)->g; }
+
 // Split K for narrow layers: up to 128 tokens, when the 128-row tiles fill at
 // most half of the SMs, K is split into as many parts as keep one unit per SM
 // (at most 8).  The workspace holds the fp32 partials of every tile at 128

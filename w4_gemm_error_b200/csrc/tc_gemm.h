@@ -35,6 +35,14 @@ cudaError_t launch_prepass_q8(const Packed &pk, const void *xq, int64_t ldx, con
                               float *v, const PrepassQ8Work &w, cudaStream_t st, int num_sms, unsigned *ready,
                               unsigned *expected);
 
+// The prepass of the forms kEpi and kQ8 on the tensor cores, K split over a
+// cluster (tc_prepass.cu).  xs and rowc: kQ8 alone; v: with `ec` alone; g: the
+// tensor map of G; ready, expected: as launch_prepass_q8.
+cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, const float *xs, int64_t M, bool ec,
+                               float *v, float *rowc, int form, const CUtensorMap *g, int *status, cudaStream_t st,
+                               int num_sms, unsigned *ready, unsigned *expected);
+const CUtensorMap *tc_map_g(const TcWork &w);   // (of a packed layer with an EC)
+
 bool tc_available(const Packed &pk);
 cudaError_t tc_alloc(const Packed &pk, int64_t max_M, int num_sms, TcWork &w);
 void tc_free(TcWork &w);

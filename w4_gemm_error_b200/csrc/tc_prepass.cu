@@ -1,0 +1,320 @@
+// Gate and EC down-projection of many tokens on the tensor cores, K split over
+// a cluster: what the forms kEpi and kQ8 of the forward pass need of each token
+// before their epilogue (see prepass.cu and prepass_q8.cu for the formulas).
+//
+//   D[t, j] = x[t,:] . G[j,:],  G = [w_g; A^T] (R1p rows)
+//   kEpi: v = g D[t,1+j],         g = 1 / (1 + exp(-(D[t,0] + b_g)))
+//   kQ8:  v = 2^-9 g D[t,1+j],    g = 1 / (1 + exp(-(xs[t] D[t,0] + b_g))),
+//         rowc: 2^9 xs[t] and 2^-9 X_t,  X_t = sum_k xq[t,k]
+//   (v rounded to tf32)
+//
+// A cluster of S CTAs takes 128 tokens; CTA q the 64-k blocks q, q + S, ...
+// The tokens are the 128 rows (TMEM lanes) of the MMA and the rows of G its N.
+// One CTA a tile leaves most SMs idle (16 of them work at 2048 tokens, 29 us);
+// S = 8 there takes under a third of it.  e4m3 activations are made bf16 on
+// their way from the copied tile to the MMA's (exact), by the same four warps
+// that later read the accumulator, which sum X_t as they go.  The S partial
+// accumulators meet in shared memory: CTA q sums its 128 / S tokens over the
+// cluster in rank order (run-to-run identical), forms the gate and writes v.
+#include <algorithm>
+
+#include "async_utils.cuh"
+#include "epilogue.cuh"
+#include "tc_gemm.h"
+#include "tensor_map.h"
+
+namespace spear {
+namespace {
+
+constexpr int kTok = 128;
+constexpr int kStages = 4;
+constexpr int kThreads = 192;
+constexpr int kMaxCluster = 8;
+
+struct TcPrepass2Params {
+    int64_t M;
+    int n_k;              // 64-k blocks
+    int S;                // CTAs a cluster
+    int R1p, r, rp;
+    float b_g;
+    const float *xs;      // kQ8
+    float *v;             // [M][rp]; null without the EC (kQ8: the code sums alone)
+    float *rowc;          // kQ8
+    int *status;
+    unsigned *ready;      // counted (release) once per CTA; null for none
+};
+
+template <int FORM>
+__host__ __device__ constexpr uint32_t xin_bytes() { return FORM == kQ8 ? kTok * 64 : 0; }
+
+// Stage: the MMA's tile of x (16 KB), the copied e4m3 tile (kQ8), the rows of G.
+template <int FORM>
+__host__ __device__ inline uint32_t stage_bytes(int R1p)
+{
+    return kTok * 128 + xin_bytes<FORM>() + (((uint32_t)R1p * 128 + 1023u) & ~1023u);
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kThreads, 1)
+tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_g,
+                   TcPrepass2Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    // copied, staged (converted) and empty of each stage; accumulator done; drain
+    __shared__ __align__(8) uint64_t bars[3 * kStages + 2];
+    __shared__ uint32_t tmem_base_slot;
+    __shared__ volatile int abort_flag;
+    __shared__ float s_gate[kTok];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t *const bp = smem_raw + (base - smem_addr(smem_raw));
+    const uint32_t full0 = smem_addr(&bars[0]), staged0 = smem_addr(&bars[kStages]);
+    const uint32_t empty0 = smem_addr(&bars[2 * kStages]);
+    const uint32_t done = smem_addr(&bars[3 * kStages]), drain = smem_addr(&bars[3 * kStages + 1]);
+    const uint32_t g_bytes = (uint32_t)p.R1p * 128, sbytes = stage_bytes<FORM>(p.R1p);
+    constexpr uint32_t kXin = kTok * 128;                 // offset of the copied e4m3 tile
+    const uint32_t o_g = kTok * 128 + xin_bytes<FORM>();  // offset of the rows of G
+    const int S = p.S, rank = S > 1 ? (int)cluster_ctarank() : 0;
+    const int t0 = (int)(blockIdx.x / S) * kTok;
+    const int nkb = (p.n_k - rank + S - 1) / S;   // this CTA's blocks (at least one)
+    const bool mma = p.R1p > 0;
+    uint32_t tmem_cols = 32;
+    while (tmem_cols < (uint32_t)p.R1p)
+        tmem_cols <<= 1;
+
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(staged0 + 8 * s, 4);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(done, 1);
+        mbar_init(drain, 1);
+        fence_mbarrier_init_cluster();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(&tmem_base_slot)),
+                     "r"(tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_slot;
+    pdl_wait();   // x and xs come from earlier kernels in the stream
+    // the next kernel may start: x is complete (it may read x without waiting)
+    // and this CTA holds its tensor memory
+    pdl_launch_dependents();
+
+    float xsum = 0.f;
+    const int q = warp & 3, row = 32 * q + lane;   // warps 2-5: TMEM lane = token of the tile
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int i = 0; i < nkb; ++i, ++issued) {
+                const uint32_t slot = i % kStages, phase = (i / kStages) & 1;
+                if (!mbar_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status))
+                    break;
+                const uint32_t sb = base + slot * sbytes, full = full0 + 8 * slot;
+                const int k = (rank + i * S) * 64;
+                mbar_expect_tx(full, (FORM == kQ8 ? xin_bytes<FORM>() : kTok * 128) + g_bytes);
+                tma_load_2d(FORM == kQ8 ? sb + kXin : sb, &tm_x, k, t0, full);
+                if (mma)
+                    tma_load_2d(sb + o_g, &tm_g, k, 0, full);
+            }
+            if (abort_flag)
+                for (int j = 0; j < kStages && j < issued; ++j) {
+                    const int i = issued - 1 - j;
+                    mbar_wait_final(full0 + 8 * (i % kStages), (i / kStages) & 1);
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.R1p >> 3) << 17) |
+                                   ((uint32_t)(kTok >> 4) << 24);
+            bool ok = true;
+            for (int i = 0; i < nkb && ok; ++i) {
+                const uint32_t slot = i % kStages, phase = (i / kStages) & 1;
+                if (!mbar_wait((FORM == kQ8 ? staged0 : full0) + 8 * slot, phase, &abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sb = base + slot * sbytes;
+                const uint64_t a_desc = smem_desc_sw128(sb), b_desc = smem_desc_sw128(sb + o_g);
+                if (mma)
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, (i > 0 || k > 0) ? 1u : 0u);
+                mma_commit(empty0 + 8 * slot);
+            }
+            if (ok)
+                mma_commit(done);
+            mma_commit(drain);
+            mbar_wait_final(drain, 0);
+        }
+    } else if (FORM == kQ8) {
+        // e4m3 -> bf16: one token's 64 k a thread
+        for (int i = 0; i < nkb; ++i) {
+            const uint32_t slot = i % kStages, phase = (i / kStages) & 1;
+            if (!mbar_wait(full0 + 8 * slot, phase, &abort_flag, p.status))
+                break;
+            uint8_t *const sb = bp + slot * sbytes;
+            const uint8_t *src = sb + kXin + row * 64;
+            uint8_t *dst = sb + row * 128;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ ((row >> 1) & 3)) << 4));
+                const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    o[2 * h] = f16x2_to_bf16x2(e4m3x2_to_f16x2((uint16_t)words[h]));
+                    o[2 * h + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2((uint16_t)(words[h] >> 16)));
+                }
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+                    xsum += bf16_lo(o[h]) + bf16_hi(o[h]);
+                *reinterpret_cast<uint4 *>(dst + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(dst + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(staged0 + 8 * slot);
+        }
+    }
+
+    // ---- this CTA's partial: [token][R1p columns of D, X], odd row length (banks)
+    const int ld = p.R1p + 1;
+    float *const part = reinterpret_cast<float *>(bp);
+    const bool got = warp < 2 || mbar_wait(done, 0, &abort_flag, p.status);
+    __syncthreads();   // every copy and MMA of this CTA is over: the stages are free
+    if (warp >= 2) {
+        tc_fence_after();
+        __syncwarp();
+        for (int c = 0; c < p.R1p; c += 16) {
+            uint32_t a[16];
+            tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * q) << 16) + c, a);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                part[row * ld + c + j] = got ? __uint_as_float(a[j]) : 0.f;
+        }
+        part[row * ld + p.R1p] = xsum;
+    }
+    if (S > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+
+    // ---- the cluster's sums of this CTA's tokens
+    const int per = kTok / S, first = rank * per;
+    auto total = [&](int tt, int j) {
+        if (S == 1)
+            return part[(first + tt) * ld + j];
+        const uint32_t a = base + (uint32_t)(((first + tt) * ld + j) * 4);
+        float v[kMaxCluster];
+#pragma unroll
+        for (int s = 0; s < kMaxCluster; ++s)
+            v[s] = s < S ? ld_dsmem_f32(map_to_rank(a, (uint32_t)s)) : 0.f;
+        float sum = v[0];
+#pragma unroll
+        for (int s = 1; s < kMaxCluster; ++s)
+            if (s < S)
+                sum += v[s];
+        return sum;
+    };
+    if (tid < per && t0 + first + tid < p.M) {
+        const int64_t t = t0 + first + tid;
+        float xs = 1.f;
+        if constexpr (FORM == kQ8) {
+            xs = __ldg(p.xs + t);
+            p.rowc[rowc_at(t)] = 512.0f * xs;
+            p.rowc[rowc_at(t) + 2] = total(tid, p.R1p) * (1.0f / 512.0f);
+        }
+        if (mma)
+            s_gate[tid] = 1.0f / (1.0f + expf(-(xs * total(tid, 0) + p.b_g))) * (FORM == kQ8 ? 1.0f / 512.0f : 1.0f);
+    }
+    __syncthreads();
+    if (mma)
+        for (int e = tid; e < per * p.rp; e += kThreads) {
+            const int tt = e / p.rp, j = e - tt * p.rp;
+            const int64_t t = t0 + first + tt;
+            if (t < p.M)
+                p.v[t * p.rp + j] = j < p.r ? to_tf32(s_gate[tt] * total(tt, 1 + j)) : 0.f;
+        }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && p.ready)
+        red_release_gpu_add(p.ready, 1u);   // this CTA's v and rowc are written
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
+    }
+    if (S > 1)
+        cluster_sync();   // no CTA leaves while another reads its partial
+}
+
+}  // namespace
+
+cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, const float *xs, int64_t M, bool ec,
+                               float *v, float *rowc, int form, const CUtensorMap *g, int *status, cudaStream_t st,
+                               int num_sms, unsigned *ready, unsigned *expected)
+{
+    const bool q8 = form == kQ8;
+    const uint64_t xd[2] = {(uint64_t)pk.K, (uint64_t)M};
+    const uint64_t xst[1] = {(uint64_t)ldx * (q8 ? 1u : 2u)};
+    const uint32_t xb[2] = {64, kTok};
+    CUtensorMap tm_x;
+    cudaError_t e = make_map_nd(&tm_x, x, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, xd,
+                                xst, xb, q8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess)
+        return e;
+    TcPrepass2Params p;
+    p.M = M;
+    p.n_k = (int)(pk.Kp / 64);   // (a multiple of 4)
+    p.R1p = ec ? pk.R1p : 0;
+    p.r = pk.r;
+    p.rp = pk.rp;
+    p.b_g = pk.b_g;
+    p.xs = xs;
+    p.v = v;
+    p.rowc = rowc;
+    p.status = status;
+    p.ready = ready;
+    const int64_t tiles = (M + kTok - 1) / kTok;
+    int S = 1;
+    while (S < kMaxCluster && 2 * S <= p.n_k && tiles * 2 * S <= num_sms)
+        S *= 2;
+    p.S = S;
+    if (expected)
+        *expected = (unsigned)(tiles * S);
+    const size_t ring = (size_t)kStages * (q8 ? stage_bytes<kQ8>(p.R1p) : stage_bytes<kEpi>(p.R1p));
+    const size_t part = (size_t)kTok * (p.R1p + 1) * sizeof(float);
+    const size_t smem = std::max(ring, part) + 1024;
+    using Fn = void (*)(CUtensorMap, CUtensorMap, TcPrepass2Params);
+    const Fn fn = q8 ? tc_prepass2_kernel<kQ8> : tc_prepass2_kernel<kEpi>;
+    e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * S));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)S;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fn, tm_x, p.R1p ? *g : tm_x, p);
+}
+
+}  // namespace spear
