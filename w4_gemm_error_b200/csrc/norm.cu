@@ -10,15 +10,18 @@
 // (the quantisation alone: v = x).  The rows feed the W4 layers: y the bf16
 // forward, (q, s) the 8-bit one.
 //
-// One CTA per row, the row in registers: it is read once and both outputs are
-// formed from the copy held there.  rinv_t is one positive factor of the whole
+// A row is read once and held in registers as h in bf16 (exact); both outputs
+// are formed from it.  rinv_t is one positive factor of the whole
 // row, so max_k |v| = rinv_t max_k |h w| (rounding is monotonic: the largest
 // product stays the largest), and the sum of squares and the maximum share one
 // block reduction: one barrier between the last load and the first store.
 // All sums are fp32; v is rounded once to each output type.
 #include <cuda_runtime.h>
 
-#include "device_utils.cuh"
+#include <algorithm>
+
+#include "async_utils.cuh"
+#include "kernels.h"
 #include "handle.h"
 #include "norm.h"
 #include "spear_w4ec.h"
@@ -41,38 +44,58 @@ struct NormParams {
     int64_t K;
 };
 
-// VEC consecutive elements from global memory, as bf16 bit patterns.
+// VEC consecutive bf16 elements (8, 2 or 1) as packed pairs.
 template <int VEC>
-__device__ __forceinline__ void load_vec(const uint16_t *p, uint16_t (&e)[VEC])
+struct Vec {
+    uint32_t w[(VEC + 1) / 2];
+    __device__ __forceinline__ float get(int i) const { return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]); }
+};
+
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> load_vec(const uint16_t *p)
 {
+    Vec<VEC> v;
     if constexpr (VEC == 8) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            e[2 * i] = (uint16_t)w[i];
-            e[2 * i + 1] = (uint16_t)(w[i] >> 16);
-        }
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
     } else if constexpr (VEC == 2) {
-        const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
-        e[0] = (uint16_t)v;
-        e[1] = (uint16_t)(v >> 16);
+        v.w[0] = *reinterpret_cast<const uint32_t *>(p);
     } else {
-        e[0] = *p;
+        v.w[0] = *p;
     }
+    return v;
 }
 
 template <int VEC>
-__device__ __forceinline__ void store_bf16(uint16_t *p, const float (&v)[VEC])
+__device__ __forceinline__ void store_vec(uint16_t *p, const Vec<VEC> &v)
 {
-    if constexpr (VEC == 8) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    } else if constexpr (VEC == 2) {
-        *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(v[0], v[1]);
-    } else {
-        *p = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
-    }
+    if constexpr (VEC == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    else if constexpr (VEC == 2)
+        *reinterpret_cast<uint32_t *>(p) = v.w[0];
+    else
+        *p = (uint16_t)v.w[0];
+}
+
+// bf16(a + b), element by element.
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> add_vec(const Vec<VEC> &a, const Vec<VEC> &b)
+{
+    Vec<VEC> v;
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i)
+        v.w[i] = pack_bf16x2(bf16_lo(a.w[i]) + bf16_lo(b.w[i]), bf16_hi(a.w[i]) + bf16_hi(b.w[i]));
+    return v;
+}
+
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> to_bf16(const float (&v)[VEC])
+{
+    Vec<VEC> o;
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i)
+        o.w[i] = pack_bf16x2(v[2 * i], 2 * i + 1 < VEC ? v[(2 * i + 1) % VEC] : 0.f);
+    return o;
 }
 
 template <int VEC>
@@ -89,158 +112,309 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[VEC])
     }
 }
 
-__device__ __forceinline__ float bf16_f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-
 // Sum and maximum over the CTA, the same in every thread.  The maximum is of
 // non-negative values (or NaN) as bit patterns: unsigned order keeps a NaN,
 // which is above every number, so that a bad row is seen.
-__device__ __forceinline__ void block_reduce(float &sum, uint32_t &top)
+struct Reduce {
+    float sum[32];
+    uint32_t top[32];
+};
+__device__ __forceinline__ void block_reduce(float &sum, float &most, Reduce &s)
 {
-    __shared__ float s_sum[32];
-    __shared__ uint32_t s_top[32];
+    uint32_t top = __float_as_uint(most) & 0x7FFFFFFFu;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (int)(blockDim.x >> 5);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, d);
     top = __reduce_max_sync(0xffffffffu, top);
+    most = __uint_as_float(top);
     if (nw == 1)
         return;
     if (lane == 0) {
-        s_sum[warp] = sum;
-        s_top[warp] = top;
+        s.sum[warp] = sum;
+        s.top[warp] = top;
     }
     __syncthreads();
-    sum = lane < nw ? s_sum[lane] : 0.f;
-    top = lane < nw ? s_top[lane] : 0u;
+    sum = lane < nw ? s.sum[lane] : 0.f;
+    top = lane < nw ? s.top[lane] : 0u;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    top = __reduce_max_sync(0xffffffffu, top);
+    most = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
 }
 
+// h w of one vector (h itself without a norm), in fp32.
+template <int VEC, bool NORM>
+__device__ __forceinline__ void times_w(const Vec<VEC> &h, const Vec<VEC> &w, float (&v)[VEC])
+{
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        v[i] = NORM ? h.get(i) * w.get(i) : h.get(i);
+}
+
+// max(|a|, |b|); NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+    return d;
+}
+
+// One vector's share of the row's statistics: the sum of h^2 and the largest
+// |h w| (needed for a quantised output alone).
+template <int VEC, bool NORM>
+__device__ __forceinline__ void count(const Vec<VEC> &h, const Vec<VEC> &w, bool q8, float &sum, float &top)
+{
+    if (NORM) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            sum += h.get(i) * h.get(i);
+    }
+    if (!q8)
+        return;
+    float v[VEC];
+    times_w<VEC, NORM>(h, w, v);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        top = max_abs(top, v[i]);
+}
+
+// The row's factors from its statistics: 1 / rms (1 without a norm), the
+// quantisation's a and 448 / a.
+struct Factors {
+    float rinv, a, inv;
+};
+template <bool NORM>
+__device__ __forceinline__ Factors factors(const NormParams &p, float sum, float top)
+{
+    Factors f;
+    f.rinv = NORM ? rsqrtf(sum / (float)p.K + p.eps) : 1.0f;   // (2 ulp)
+    const uint32_t amax = __float_as_uint(top * f.rinv) & 0x7FFFFFFFu;
+    f.a = __uint_as_float(max(amax, __float_as_uint(kAmaxFloor)));
+    f.inv = kE4m3Max / f.a;
+    return f;
+}
+
+template <int VEC, bool NORM>
+__device__ __forceinline__ void emit(const NormParams &p, int64_t at, const Vec<VEC> &h, const Vec<VEC> &w,
+                                     const Factors &f)
+{
+    float v[VEC];
+    times_w<VEC, NORM>(h, w, v);
+    if (NORM) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            v[i] *= f.rinv;
+    }
+    if (NORM && p.y)
+        store_vec<VEC>(p.y + at, to_bf16<VEC>(v));
+    if (p.q) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            v[i] *= f.inv;
+        store_e4m3<VEC>(p.q + at, v);
+    }
+}
+
+// ---- one CTA a row: few rows, rows that are no multiple of 8 elements, or
+// rows too long for the pipelined kernel below.
 // NV vectors of VEC elements a thread; NV = 0: the row is longer than the
-// registers hold and is read again for the outputs (h is rounded the same way
-// both times; a sum stored over its residual is read back from h instead).
-template <int VEC, int NV>
+// registers hold and is read again for the outputs (a sum that was stored is
+// read back, since x or the residual may be the same memory).
+template <int VEC, int NV, bool NORM>
 __global__ void __launch_bounds__(1024) norm_kernel(NormParams p)
 {
+    __shared__ Reduce s_red;
     pdl_launch_dependents();
     pdl_wait();   // every operand may come from an earlier kernel in the stream
-    const int64_t row = blockIdx.x;
+    const int64_t at = (int64_t)blockIdx.x * p.K;
     const int T = (int)blockDim.x, tid = (int)threadIdx.x;
     const int64_t nvec = p.K / VEC;
-    const uint16_t *x = p.x + row * p.K;
-    const uint16_t *res = p.residual ? p.residual + row * p.K : nullptr;
-    uint16_t *h = p.h ? p.h + row * p.K : nullptr;
-    constexpr bool kHeld = NV > 0;
-    constexpr int kN = kHeld ? NV : 1;
-    float hv[kN][VEC];   // h, then h w
+    const bool q8 = p.q != nullptr;
+    constexpr int kN = NV > 0 ? NV : 1;
+    Vec<VEC> h[kN] = {}, w[kN] = {};
     float sum = 0.f;
-    uint32_t top = 0u;
-
-    auto load_h = [&](int64_t c, float (&v)[VEC]) {
-        uint16_t e[VEC];
-        load_vec<VEC>(x + c * VEC, e);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            v[i] = bf16_f(e[i]);
-        if (res) {
-            load_vec<VEC>(res + c * VEC, e);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                v[i] = __bfloat162float(__float2bfloat16_rn(v[i] + bf16_f(e[i])));
-        }
+    float top = 0.f;
+    auto load_h = [&](int64_t c) {
+        Vec<VEC> v = load_vec<VEC>(p.x + at + c * VEC);
+        if (p.residual)
+            v = add_vec<VEC>(v, load_vec<VEC>(p.residual + at + c * VEC));
+        return v;
     };
-    auto times_w = [&](int64_t c, float (&v)[VEC]) {
-        if (!p.w)
-            return;
-        uint16_t e[VEC];
-        load_vec<VEC>(p.w + c * VEC, e);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            v[i] *= bf16_f(e[i]);
-    };
-    auto count = [&](int64_t c, float (&v)[VEC]) {
-        if (h)
-            store_bf16<VEC>(h + c * VEC, v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            sum += v[i] * v[i];
-        times_w(c, v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            top = max(top, __float_as_uint(fabsf(v[i])));
-    };
-    if constexpr (kHeld) {
+    if constexpr (NV > 0) {
+        // every load is issued before the first is used
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = tid + (int64_t)j * T;
             if (c < nvec) {
-                load_h(c, hv[j]);
-                count(c, hv[j]);
+                h[j] = load_h(c);
+                if (NORM)
+                    w[j] = load_vec<VEC>(p.w + c * VEC);
             }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {   // (a vector past the row is zero and counts for nothing)
+            const int64_t c = tid + (int64_t)j * T;
+            if (p.h && c < nvec)
+                store_vec<VEC>(p.h + at + c * VEC, h[j]);
+            count<VEC, NORM>(h[j], w[j], q8, sum, top);
         }
     } else {
         for (int64_t c = tid; c < nvec; c += T) {
-            load_h(c, hv[0]);
-            count(c, hv[0]);
+            h[0] = load_h(c);
+            if (NORM)
+                w[0] = load_vec<VEC>(p.w + c * VEC);
+            if (p.h)
+                store_vec<VEC>(p.h + at + c * VEC, h[0]);
+            count<VEC, NORM>(h[0], w[0], q8, sum, top);
         }
     }
-    block_reduce(sum, top);
-    const float rinv = p.w ? 1.0f / sqrtf(sum / (float)p.K + p.eps) : 1.0f;
-    uint32_t amax = __float_as_uint(__uint_as_float(top) * rinv);
-    amax = max(amax & 0x7FFFFFFFu, __float_as_uint(kAmaxFloor));
-    const float a = __uint_as_float(amax);
-    const float inv = kE4m3Max / a;
-    if (p.q && tid == 0)
-        p.s[row] = a / kE4m3Max;
-    auto emit = [&](int64_t c, float (&v)[VEC]) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            v[i] *= rinv;
-        if (p.y)
-            store_bf16<VEC>(p.y + row * p.K + c * VEC, v);
-        if (p.q) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                v[i] *= inv;
-            store_e4m3<VEC>(p.q + row * p.K + c * VEC, v);
-        }
-    };
-    if constexpr (kHeld) {
+    block_reduce(sum, top, s_red);
+    const Factors f = factors<NORM>(p, sum, top);
+    if (q8 && tid == 0)
+        p.s[blockIdx.x] = f.a / kE4m3Max;
+    if constexpr (NV > 0) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int64_t c = tid + (int64_t)j * T;
             if (c < nvec)
-                emit(c, hv[j]);
+                emit<VEC, NORM>(p, at + c * VEC, h[j], w[j], f);
         }
     } else {
         for (int64_t c = tid; c < nvec; c += T) {
-            if (h) {   // written above by this thread; x or the residual may be the same memory
-                uint16_t e[VEC];
-                load_vec<VEC>(h + c * VEC, e);
+            h[0] = p.h ? load_vec<VEC>(p.h + at + c * VEC) : load_h(c);
+            if (NORM)
+                w[0] = load_vec<VEC>(p.w + c * VEC);
+            emit<VEC, NORM>(p, at + c * VEC, h[0], w[0], f);
+        }
+    }
+}
+
+// ---- many rows: persistent CTAs, each with a ring of rows in shared memory
+// filled by bulk copies.  HBM bounds this case; with one CTA a row an SM's
+// loads pause while its CTAs reduce and store, and every CTA pays its launch
+// (2047 rows of 14336 quantised: 30 us, 2.9 TB/s).  Here the copies of the next
+// rows are in flight throughout, and the weights stay in registers.
+constexpr int kRing = 4;   // rows of the ring at most
+// CTAs an SM holds (of 512 threads with four vectors a thread, else of 256): as
+// many as the registers allow without spills, since a CTA's own chain (wait,
+// statistics, barrier, outputs) is latency and only other CTAs fill it.
+__host__ __device__ constexpr int rows_per_sm(int nv, bool norm) { return nv == 4 ? (norm ? 2 : 3) : (norm ? 5 : 6); }
+
+template <int NV, bool NORM>
+__global__ void __launch_bounds__(NV == 4 ? 512 : 256, rows_per_sm(NV, NORM)) norm_rows_kernel(NormParams p, int64_t M, int ring)
+{
+    extern __shared__ __align__(128) uint8_t rows[];   // [ring][x row, residual row]
+    __shared__ Reduce s_red[2];
+    __shared__ __align__(8) uint64_t bars[kRing];
+    const int T = (int)blockDim.x, tid = (int)threadIdx.x;
+    const int nvec = (int)(p.K / 8);
+    const uint32_t row_bytes = (uint32_t)p.K * 2, stage_bytes = row_bytes * (p.residual ? 2 : 1);
+    const bool q8 = p.q != nullptr;
+    if (tid == 0) {
+        for (int s = 0; s < ring; ++s)
+            mbar_init(smem_addr(&bars[s]), 1);
+        fence_mbarrier_init_cluster();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    pdl_wait();   // every operand may come from an earlier kernel in the stream
+    auto request = [&](int64_t t, int s) {
+        const uint32_t bar = smem_addr(&bars[s]), dst = smem_addr(rows) + (uint32_t)s * stage_bytes;
+        mbar_expect_tx(bar, stage_bytes);
+        bulk_load(dst, p.x + t * p.K, row_bytes, bar);
+        if (p.residual)
+            bulk_load(dst + row_bytes, p.residual + t * p.K, row_bytes, bar);
+    };
+    if (tid == 0)
+        for (int s = 0; s < ring; ++s)
+            if (blockIdx.x + (int64_t)s * gridDim.x < M)
+                request(blockIdx.x + (int64_t)s * gridDim.x, s);
+    Vec<8> w[NV] = {};
+    if (NORM) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    hv[0][i] = bf16_f(e[i]);
-            } else {
-                load_h(c, hv[0]);
+        for (int j = 0; j < NV; ++j)
+            if (tid + j * T < nvec)
+                w[j] = load_vec<8>(p.w + (int64_t)(tid + j * T) * 8);
+    }
+    int s = 0, prev = -1, round = 0;
+    uint32_t phase = 0;
+    for (int64_t t = blockIdx.x; t < M; t += gridDim.x, ++round) {
+        // a copy that never lands (bounded wait) leaves NaN in its row
+        const bool landed = mbar_wait_bounded(smem_addr(&bars[s]), phase);
+        const uint16_t *xr = reinterpret_cast<const uint16_t *>(rows + (size_t)s * stage_bytes);
+        Vec<8> h[NV] = {};
+        float sum = 0.f;
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = tid + j * T;
+            if (c < nvec) {
+                h[j] = load_vec<8>(xr + c * 8);
+                if (p.residual)
+                    h[j] = add_vec<8>(h[j], load_vec<8>(xr + p.K + c * 8));
+                if (p.h)
+                    store_vec<8>(p.h + t * p.K + (int64_t)c * 8, h[j]);
             }
-            times_w(c, hv[0]);
-            emit(c, hv[0]);
+            count<8, NORM>(h[j], w[j], q8, sum, top);
+        }
+        if (!landed)
+            sum = top = __int_as_float(0x7FFFFFFF);
+        block_reduce(sum, top, s_red[round & 1]);
+        // (every thread has read the row: its stage can take the row `ring` rounds on;
+        // a CTA of one warp has no barrier in its reduction)
+        if (T == 32)
+            __syncwarp();
+        prev = s;
+        if (++s == ring) {
+            s = 0;
+            phase ^= 1u;
+        }
+        if (tid == 0 && t + (int64_t)ring * gridDim.x < M)
+            request(t + (int64_t)ring * gridDim.x, prev);
+        const Factors f = factors<NORM>(p, sum, top);
+        if (q8 && tid == 0)
+            p.s[t] = f.a / kE4m3Max;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = tid + j * T;
+            if (c < nvec)
+                emit<8, NORM>(p, t * p.K + (int64_t)c * 8, h[j], w[j], f);
         }
     }
 }
 
 using NormFn = void (*)(NormParams);
-template <int VEC>
+template <int VEC, bool NORM>
 NormFn norm_fn(int nv)
 {
     switch (nv) {
-    case 1: return norm_kernel<VEC, 1>;
-    case 2: return norm_kernel<VEC, 2>;
-    case 4: return norm_kernel<VEC, 4>;
-    default: return norm_kernel<VEC, 0>;
+    case 1: return norm_kernel<VEC, 1, NORM>;
+    case 2: return norm_kernel<VEC, 2, NORM>;
+    case 4: return norm_kernel<VEC, 4, NORM>;
+    default: return norm_kernel<VEC, 0, NORM>;
     }
+}
+
+using NormRowsFn = void (*)(NormParams, int64_t, int);
+template <bool NORM>
+NormRowsFn norm_rows_fn(int nv)
+{
+    switch (nv) {
+    case 1: return norm_rows_kernel<1, NORM>;
+    case 2: return norm_rows_kernel<2, NORM>;
+    default: return norm_rows_kernel<4, NORM>;
+    }
+}
+
+// SMs of the current device.
+int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
 }
 
 }  // namespace
@@ -260,6 +434,13 @@ cudaError_t launch_norm(const void *x, const void *residual, const void *w, floa
     p.q = static_cast<uint8_t *>(q);
     p.s = s;
     p.K = K;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     // the widest access that every row starts on (the bases are 16-byte aligned)
     const int vec = K % 8 == 0 ? 8 : (K % 2 == 0 ? 2 : 1);
     const int64_t nvec = K / vec;
@@ -268,20 +449,36 @@ cudaError_t launch_norm(const void *x, const void *residual, const void *w, floa
         nv *= 2;
     int64_t threads = (nvec + nv - 1) / nv;
     threads = (threads + 31) / 32 * 32;
+    // many rows: the pipelined kernel, when an SM's shared memory holds at least
+    // two rows of two CTAs (or three of one) and each CTA has several rows
+    const int sms = vec == 8 && threads <= 512 && M >= 4 * 148 ? sm_count() : 0;
+    if (sms > 0) {
+        const size_t stage = (size_t)K * 2 * (residual ? 2 : 1);
+        const size_t room = 220 * 1024;
+        int per_sm = (int)std::min<int64_t>(16, rows_per_sm(nv, w != nullptr) * (nv == 4 ? 512 : 256) / threads);
+        while (per_sm > 1 && room / per_sm < 2 * stage + 1024)
+            --per_sm;
+        const int ring = (int)std::min<size_t>(kRing, (room / per_sm - 1024) / stage);
+        if (ring >= (per_sm > 1 ? 2 : 3)) {
+            const NormRowsFn fn = w ? norm_rows_fn<true>(nv) : norm_rows_fn<false>(nv);
+            const size_t smem = ring * stage;
+            const cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
+            if (e != cudaSuccess)
+                return e;
+            cfg.gridDim = dim3((unsigned)std::min<int64_t>(M, (int64_t)per_sm * sms));
+            cfg.blockDim = dim3((unsigned)threads);
+            cfg.dynamicSmemBytes = smem;
+            return cudaLaunchKernelEx(&cfg, fn, p, M, ring);
+        }
+    }
     if (threads > 1024) {
         threads = 1024;
         nv = 0;
     }
-    NormFn fn = vec == 8 ? norm_fn<8>(nv) : (vec == 2 ? norm_fn<2>(nv) : norm_fn<1>(nv));
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)M);
     cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const NormFn fn = w ? (vec == 8 ? norm_fn<8, true>(nv) : (vec == 2 ? norm_fn<2, true>(nv) : norm_fn<1, true>(nv)))
+                        : (vec == 8 ? norm_fn<8, false>(nv) : (vec == 2 ? norm_fn<2, false>(nv) : norm_fn<1, false>(nv)));
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 

@@ -350,41 +350,48 @@ def spear_w4ec_tp_destroy(t: int):
     _check(_lib.spear_w4ec_tp_destroy(t), "spear_w4ec_tp_destroy")
 
 
-def _dev(t: torch.Tensor, dtype, shape, name, device):
-    """t's address, after checking its type, shape, layout and device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t.data_ptr()
+def _dev(t, dtype, shape, name, index):
+    """t's address, after checking its type, shape, layout and device (a few
+    attribute reads: the small calls last no longer than their checks do)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
 
 
 def _cuda_rows(x, name):
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2):
+    """(M, K, device index) of a CUDA tensor [M, K]."""
+    try:
+        M, K = x.shape
+        index = x.get_device()
+    except (AttributeError, ValueError):
+        index = -1
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor [M, K]")
-    return x.shape[0], x.shape[1], x.device
+    return M, K, index
 
 
-def _stream_on(stream, device) -> int:
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_on(stream, index) -> int:
     """The given stream's handle, or that of the device's current stream."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _raw_stream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-class _on:
-    """Makes a tensor's device current for a call that runs on the current one."""
-
-    def __init__(self, device):
-        self.device = device
-
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.device.index:
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.prev != self.device.index:
-            torch.cuda.set_device(self.prev)
+def _call_on(index, f, call, *args):
+    """f(*args) with device `index` current (for calls that run on the current device)."""
+    if torch._C._cuda_getDevice() == index:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args)
+    if rc:
+        raise SpearError(rc, call)
 
 
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None, *,
@@ -396,30 +403,30 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
     y is the norm in bf16 (``bf16``); q, s are the norm in float8_e4m3fn with
     one float32 scale a row (``q8``), as W4ECLinear.forward_q8 takes them;
     h = bf16(x + residual), of which the norm is taken, with a residual.  The
-    ``out*`` tensors are written where given (h may be x or residual itself),
-    else new ones."""
+    ``out*`` tensors are written where given (h and y may be x or residual
+    itself), else new ones."""
     M, K, dev = _cuda_rows(x, "x")
     if not (bf16 or q8):
         raise ValueError("at least one of bf16 and q8 must be asked for")
     if (out is not None and not bf16) or (not q8 and (out_q is not None or out_s is not None)) or \
             (residual is None and out_sum is not None):
         raise ValueError("an output tensor was given for an output that was not asked for")
-    px, pw = _dev(x, torch.bfloat16, (M, K), "x", dev), _dev(weight, torch.bfloat16, (K,), "weight", dev)
+    rows, tb = (M, K), torch.bfloat16
+    px, pw = _dev(x, tb, rows, "x", dev), _dev(weight, tb, (K,), "weight", dev)
     y = q = s = h = py = pq = ps = ph = pr = None
     if residual is not None:
-        pr = _dev(residual, torch.bfloat16, (M, K), "residual", dev)
+        pr = _dev(residual, tb, rows, "residual", dev)
         h = torch.empty_like(x) if out_sum is None else out_sum
-        ph = _dev(h, torch.bfloat16, (M, K), "out_sum", dev)
+        ph = _dev(h, tb, rows, "out_sum", dev)
     if bf16:
         y = torch.empty_like(x) if out is None else out
-        py = _dev(y, torch.bfloat16, (M, K), "out", dev)
+        py = _dev(y, tb, rows, "out", dev)
     if q8:
-        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if out_q is None else out_q
-        s = torch.empty(M, dtype=torch.float32, device=dev) if out_s is None else out_s
-        pq, ps = _dev(q, torch.float8_e4m3fn, (M, K), "out_q", dev), _dev(s, torch.float32, (M,), "out_s", dev)
-    with _on(dev):
-        _check(_lib.spear_w4ec_rmsnorm(px, pr, pw, eps, M, K, ph, py, pq, ps, _stream_on(stream, dev)),
-               "spear_w4ec_rmsnorm")
+        q = torch.empty(rows, dtype=torch.float8_e4m3fn, device=x.device) if out_q is None else out_q
+        s = torch.empty(M, dtype=torch.float32, device=x.device) if out_s is None else out_s
+        pq, ps = _dev(q, torch.float8_e4m3fn, rows, "out_q", dev), _dev(s, torch.float32, (M,), "out_s", dev)
+    _call_on(dev, _lib.spear_w4ec_rmsnorm, "spear_w4ec_rmsnorm", px, pr, pw, eps, M, K, ph, py, pq, ps,
+             _stream_on(stream, dev))
     return y, q, s, h
 
 
@@ -428,12 +435,12 @@ def quantize_q8(x: torch.Tensor, *, out_q: torch.Tensor | None = None, out_s: to
     """x [M, K] (bf16) in 8 bits: (q float8_e4m3fn [M, K], s float32 [M]) with
     x ~ q * s[:, None], as W4ECLinear.forward_q8 takes them."""
     M, K, dev = _cuda_rows(x, "x")
-    px = _dev(x, torch.bfloat16, (M, K), "x", dev)
-    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev) if out_q is None else out_q
-    s = torch.empty(M, dtype=torch.float32, device=dev) if out_s is None else out_s
-    pq, ps = _dev(q, torch.float8_e4m3fn, (M, K), "out_q", dev), _dev(s, torch.float32, (M,), "out_s", dev)
-    with _on(dev):
-        _check(_lib.spear_w4ec_quantize_q8(px, M, K, pq, ps, _stream_on(stream, dev)), "spear_w4ec_quantize_q8")
+    rows = (M, K)
+    px = _dev(x, torch.bfloat16, rows, "x", dev)
+    q = torch.empty(rows, dtype=torch.float8_e4m3fn, device=x.device) if out_q is None else out_q
+    s = torch.empty(M, dtype=torch.float32, device=x.device) if out_s is None else out_s
+    pq, ps = _dev(q, torch.float8_e4m3fn, rows, "out_q", dev), _dev(s, torch.float32, (M,), "out_s", dev)
+    _call_on(dev, _lib.spear_w4ec_quantize_q8, "spear_w4ec_quantize_q8", px, M, K, pq, ps, _stream_on(stream, dev))
     return q, s
 
 
@@ -494,14 +501,18 @@ class W4ECLinear:
     __call__ = forward
 
     def _epilogue(self, M, act, bias, mul, residual, dev):
+        """The spear_w4ec_epilogue of a call, or None for one that does nothing."""
         try:
             code = ACTIVATIONS[act]
         except (KeyError, TypeError):
             raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}") from None
-        return Epilogue(None if bias is None else _dev(bias, torch.bfloat16, (self.N,), "bias", dev),
-                        None if mul is None else _dev(mul, torch.bfloat16, (M, self.N), "mul", dev),
-                        None if residual is None else _dev(residual, torch.bfloat16, (M, self.N), "residual", dev),
-                        code, 0)
+        rows, tb = (M, self.N), torch.bfloat16
+        b = None if bias is None else _dev(bias, tb, (self.N,), "bias", dev)
+        m = None if mul is None else _dev(mul, tb, rows, "mul", dev)
+        r = None if residual is None else _dev(residual, tb, rows, "residual", dev)
+        if not (code or b or m or r):
+            return None
+        return ctypes.byref(Epilogue(b, m, r, code, 0))
 
     def forward_ep(self, x: torch.Tensor, *, act: str = "none", bias: torch.Tensor | None = None,
                    mul: torch.Tensor | None = None, residual: torch.Tensor | None = None, flags: int = 0,
@@ -511,11 +522,12 @@ class W4ECLinear:
         and residual bf16 [M, N] (each may be ``out`` itself)."""
         M, _, dev = _cuda_rows(x, "x")
         px = _dev(x, torch.bfloat16, (M, self.K), "x", dev)
-        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=dev) if out is None else out
+        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device) if out is None else out
         py = _dev(y, torch.bfloat16, (M, self.N), "out", dev)
         ep = self._epilogue(M, act, bias, mul, residual, dev)
-        _check(_lib.spear_w4ec_forward_ep(self.h, px, py, M, ctypes.byref(ep), flags, _stream_on(stream, dev)),
-               "spear_w4ec_forward_ep")
+        rc = _lib.spear_w4ec_forward_ep(self.h, px, py, M, ep, flags, _stream_on(stream, dev))
+        if rc:
+            raise SpearError(rc, "spear_w4ec_forward_ep")
         return y
 
     def forward_q8(self, xq: torch.Tensor, xs: torch.Tensor, *, act: str = "none", bias: torch.Tensor | None = None,
@@ -524,12 +536,14 @@ class W4ECLinear:
         """forward_ep on 8-bit activations x = xq * xs[:, None] (float8_e4m3fn
         [M, K] and float32 [M], as rmsnorm and quantize_q8 make them)."""
         M, _, dev = _cuda_rows(xq, "xq")
-        px, ps = _dev(xq, torch.float8_e4m3fn, (M, self.K), "xq", dev), _dev(xs, torch.float32, (M,), "xs", dev)
-        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=dev) if out is None else out
+        px = _dev(xq, torch.float8_e4m3fn, (M, self.K), "xq", dev)
+        ps = _dev(xs, torch.float32, (M,), "xs", dev)
+        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=xq.device) if out is None else out
         py = _dev(y, torch.bfloat16, (M, self.N), "out", dev)
         ep = self._epilogue(M, act, bias, mul, residual, dev)
-        _check(_lib.spear_w4ec_forward_q8(self.h, px, ps, py, M, ctypes.byref(ep), flags, _stream_on(stream, dev)),
-               "spear_w4ec_forward_q8")
+        rc = _lib.spear_w4ec_forward_q8(self.h, px, ps, py, M, ep, flags, _stream_on(stream, dev))
+        if rc:
+            raise SpearError(rc, "spear_w4ec_forward_q8")
         return y
 
     def packed(self, stream=None):
