@@ -84,6 +84,15 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void *p, uint32_t bytes)
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// A box of a tensor map from HBM into L2 (a hint, as above).
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int c0, int c1)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+}
+
 // Cross-layer weight prefetch: this CTA's share of [base, base + bytes) (a
 // multiple of 16 bytes, 16-byte aligned) read from HBM into L2, in pieces of
 // at most 32 KB.  A hint: nothing waits for it.
@@ -127,6 +136,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// A warp's wait: every lane waits, all learn the same outcome.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
 // Bounded wait without a shared abort flag: false if it runs out.
 __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity)
 {
@@ -420,6 +436,12 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ float2 ld_dsmem_f2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
 __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr)
 {
     float v;
@@ -439,6 +461,24 @@ __device__ __forceinline__ unsigned ld_acquire_gpu(const unsigned *p)
     unsigned v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
+}
+
+// Bounded wait until an earlier kernel, still running, has counted `expected`
+// releases into *counter; the copies that follow then read what it wrote.
+__device__ __forceinline__ bool wait_counted(const unsigned *counter, unsigned expected, volatile int *abort_flag,
+                                             int *status)
+{
+    const long long t0 = clock64();
+    while (ld_acquire_gpu(counter) < expected) {
+        if (*abort_flag || clock64() - t0 > kWaitBudgetCycles) {
+            *abort_flag = 1;
+            atomicOr(status, kStatusTimeout);
+            return false;
+        }
+        __nanosleep(64);
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    return true;
 }
 
 }  // namespace spear

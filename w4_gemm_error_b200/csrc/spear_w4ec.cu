@@ -172,7 +172,7 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
     const bool early = ec && fused && (choice & SPEAR_FORCE_TC) && tc_supported(h);
     unsigned expected = 0;
     if (ec && !(decode && fused)) {
-        if (form == kEpi && M >= kPairMinTokens)
+        if (form == kEpi && (choice & SPEAR_FORCE_TC))
             e = launch_tc_prepass2(pk, x, pk.K, nullptr, M, true, h->v, nullptr, kEpi, tc_map_g(h->tc), h->status, st,
                                    h->num_sms, early ? h->vready : nullptr, &expected);
         else
@@ -269,11 +269,11 @@ int run_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y
         // the prepass, which counts what it has written into vready
         unsigned expected = 0;
         unsigned *ready = ec ? h->vready : nullptr;
-        cudaError_t e = M >= kPairMinTokens
-                            ? launch_tc_prepass2(pk, xq, ldx, xs, M, ec, h->v, h->preq8.rowc, kQ8, tc_map_g(h->tc),
-                                                 h->status, st, h->num_sms, ready, &expected)
-                            : launch_prepass_q8(pk, xq, ldx, xs, M, ec, h->v, h->preq8, st, h->num_sms, ready,
-                                                &expected);
+        // (without the EC only the pair kernel needs one: the other sums the codes itself)
+        cudaError_t e = cudaSuccess;
+        if (ec || tc_use_pair(pk, M, h->num_sms))
+            e = launch_tc_prepass2(pk, xq, ldx, xs, M, ec, h->v, h->preq8.rowc, kQ8, tc_map_g(h->tc), h->status, st,
+                                   h->num_sms, ready, &expected);
         if (e != cudaSuccess)
             return from_cuda(e);
         e = launch_tc(pk, xq, y, M, h->v, ec, h->tc, h->status, h->fault_timeout, st, h->num_sms,

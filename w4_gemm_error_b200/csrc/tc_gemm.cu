@@ -767,6 +767,14 @@ cudaError_t tc_prepare(const Packed &pk, TcWork &w)
     return e;
 }
 
+// Whether the forms with an epilogue take the pair kernel: its 256 x 256 tiles
+// read half as much per product, but fill the machine from 74 of them on.
+bool tc_use_pair(const Packed &pk, int64_t M, int num_sms)
+{
+    const int64_t pairs = (M + 255) / 256 * ((pk.Np + 255) / 256);
+    return M > 128 && 4 * pairs >= num_sms;
+}
+
 namespace {
 
 using TcFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, TcParams);
@@ -798,9 +806,10 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
         const int bits = kStatusTimeout;
         return cudaMemcpyAsync(status, &bits, sizeof(int), cudaMemcpyHostToDevice, st);
     }
-    if (form != kPlain && M >= kPairMinTokens)
-        return launch_tc_pair(pk, x, y, M, v, ec, &m->bt, status, st, num_sms, v_ready, v_expected, form,
-                              epi, ldx, rowc);
+    if (form != kPlain) {
+        const auto launch = tc_use_pair(pk, M, num_sms) ? launch_tc_pair : launch_tc_tile;
+        return launch(pk, x, y, M, v, ec, &m->bt, status, st, num_sms, v_ready, v_expected, form, epi, ldx, rowc);
+    }
     // token tile: the narrowest of 32, 64, 128, 256 that holds M (one tile row of tokens
     // up to 256), so that small batches do not run 256-wide MMAs on zero rows
     const int BN = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));

@@ -65,10 +65,16 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
                       unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
                       const float *rowc);
 
-// The forms kEpi and kQ8 from kPairMinTokens tokens on (tc_pair.cu; launch_tc
-// takes it).  bt: the tensor map of B^T/e; rowc holds whole chunks of 32 tokens.
-constexpr int64_t kPairMinTokens = 129;
+// The forms kEpi and kQ8 (launch_tc takes them): pairs of CTAs on 256 x 256
+// tiles (tc_pair.cu), or one CTA on 128 x up to 128 with K split over a cluster
+// (tc_tile.cu).  bt: the tensor map of B^T/e; rowc holds whole chunks of 32
+// tokens.
+bool tc_use_pair(const Packed &pk, int64_t M, int num_sms);
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
+                           const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,
+                           unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
+                           const float *rowc);
+cudaError_t launch_tc_tile(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                            const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,
                            unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
                            const float *rowc);

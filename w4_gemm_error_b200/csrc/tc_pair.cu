@@ -43,6 +43,7 @@
 
 #include "async_utils.cuh"
 #include "epilogue.cuh"
+#include "tc_dequant.cuh"
 #include "tc_gemm.h"
 #include "tensor_map.h"
 
@@ -51,7 +52,7 @@ namespace {
 
 constexpr int BM = 128;                 // weight rows of a CTA (256 a pair)
 constexpr int BN = 256;                 // tokens of a pair (128 staged by each CTA)
-constexpr int ROW_BYTES = 128;
+constexpr int ROW_BYTES = kTcRowBytes;
 constexpr int A_BYTES = BM * ROW_BYTES;
 constexpr int B_BYTES = (BN / 2) * ROW_BYTES;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -63,7 +64,6 @@ constexpr int ROWC_BYTES = CHUNK * 8;
 constexpr int EPI_WARP = 4, DEQ_WARP = 12, GROUP_WARPS = 4, GROUPS = 4;
 constexpr int THREADS = 32 * (DEQ_WARP + GROUPS * GROUP_WARPS);
 
-__host__ __device__ constexpr int pair_bk(int form) { return form == kQ8 ? 128 : 64; }
 // Ring depth and shared memory with and without a multiplier in the slots.
 int pair_stages(bool mul) { return mul ? 5 : 6; }
 int pair_smem_bytes(bool mul)
@@ -87,29 +87,6 @@ struct PairParams {
     const float *rowc;       // form kQ8: as TcParams::rowc, padded to whole chunks
 };
 
-// Bounded wait until the prepass has counted everything it writes.
-__device__ __forceinline__ bool wait_prepass(const PairParams &p, volatile int *abort_flag)
-{
-    const long long t0 = clock64();
-    while (ld_acquire_gpu(p.v_ready) < p.v_expected) {
-        if (*abort_flag || clock64() - t0 > kWaitBudgetCycles) {
-            *abort_flag = 1;
-            atomicOr(p.status, kStatusTimeout);
-            return false;
-        }
-        __nanosleep(64);
-    }
-    asm volatile("fence.proxy.async;" ::: "memory");   // the copies that follow read what it wrote
-    return true;
-}
-
-// A warp's wait: every lane waits, all learn the same outcome.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status)
-{
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-        return true;
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
-}
 // One slot's outputs of this thread: channel n (row `row` of the CTA), the 32
 // tokens of the chunk, the accumulator at tacc in TMEM.  mul and y are its columns of
 // [32 tokens][128 channels] bf16.  Eight tokens at a time: every shared-memory
@@ -171,25 +148,13 @@ __device__ __forceinline__ void emit_chunk_of(uint32_t tacc, float e_n, float z_
                 : emit_chunk<FORM, ACT, false, false>(tacc, e_n, z_n, bias, mul, y, rc);
 }
 
-// A dequantiser thread's codes of one stage: `kPieces` 16-byte pieces, lanes
-// side by side in a row's piece so that a warp's load is whole 32-byte sectors.
-// Form kQ8 (64 bytes a row): piece lane % 4 of rows lane / 4 + 8 j; kEpi
-// (32 bytes a row): piece lane % 2 of rows lane / 2 + 16 j.
-template <int FORM>
-struct Codes {
-    static constexpr int kLanes = FORM == kQ8 ? 4 : 2;    // lanes a row
-    static constexpr int kPieces = FORM == kQ8 ? 4 : 2;   // pieces (rows) a thread
-    uint4 w[kPieces];
-};
-
 template <int FORM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_bt, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_mul, const __grid_constant__ CUtensorMap tm_res,
                const __grid_constant__ CUtensorMap tm_y, PairParams p)
 {
-    constexpr int BK = pair_bk(FORM);
-    constexpr int SUB = 256 / BK;
+    constexpr int BK = tc_stage_k(FORM);
     extern __shared__ uint8_t smem_raw[];
     // ready and empty of each stage; accumulator full and empty; slot full and empty; drain
     __shared__ __align__(8) uint64_t bars[2 * MAX_STAGES + 4 + 2 * NSLOT + 1];
@@ -274,7 +239,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         tma_load_2d_pair(sb + A_BYTES, &tm_x, i * BK, t0, ready);
                     }
                 } else {
-                    if (!v_seen && !__all_sync(0xffffffffu, wait_prepass(p, &abort_flag))) {
+                    if (!v_seen && !__all_sync(0xffffffffu, wait_counted(p.v_ready, p.v_expected, &abort_flag, p.status))) {
                         ok = false;
                         break;
                     }
@@ -393,7 +358,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         mbar_arrive(bar);
                         continue;
                     }
-                    if (!ready && !wait_prepass(p, &abort_flag)) {
+                    if (!ready && !wait_counted(p.v_ready, p.v_expected, &abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
@@ -505,26 +470,19 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             bulk_wait_all();   // the stores are complete (and the slots read) before the CTA leaves
     } else if (warp >= DEQ_WARP) {
         // ------------------------------------------------ dequantisers: group `grp` takes every fourth stage
-        using Piece = Codes<FORM>;
-        constexpr int kRowStep = 32 / Piece::kLanes;   // rows between a thread's pieces
         const int grp = (warp - DEQ_WARP) / GROUP_WARPS, w = warp & 3;
-        const int piece = lane % Piece::kLanes, r0 = 32 * w + lane / Piece::kLanes;
+        TcDequant<FORM> d(w, lane);
         // this group's stages in order, GROUPS apart: (u, st) the one at work, (fu, fst)
         // the one whose codes are fetched, `src` its unit's codes (null: none)
-        const int64_t thread_off = (int64_t)(r0 & 63) * 128 + piece * 16;
         int u = cluster, st = grp, fu = 0, fst = 0;
         const uint8_t *src = nullptr;
         auto enter = [&]() {   // the fetching side's unit is fu
             const int nb = (fu / p.n_ttiles) * 4 + (int)rank * 2 + (w >> 1);   // 64-row block of this warp's rows
             src = fu < p.n_units && (int64_t)nb * 64 < p.Np
-                      ? p.codes + (int64_t)nb * p.kchunks * 8192 + thread_off : nullptr;
+                      ? p.codes + (int64_t)nb * p.kchunks * 8192 + d.offset() : nullptr;
         };
-        auto fetch = [&](Piece &c) {   // (the codes do not depend on earlier kernels: no wait)
-            const bool some = src && fst < p.n_main;
-            const uint8_t *at = src + (int64_t)(fst / SUB) * 8192 + (fst % SUB) * (BK / 2);
-#pragma unroll
-            for (int j = 0; j < Piece::kPieces; ++j)
-                c.w[j] = some ? ld_stream(at + j * kRowStep * 128) : make_uint4(0u, 0u, 0u, 0u);
+        auto fetch = [&]() {   // (the codes do not depend on earlier kernels: no wait)
+            d.fetch(fst < p.n_main ? src : nullptr, fst);
             fst += GROUPS;
             if (fst >= nst) {
                 while (fst >= nst && fu < p.n_units) {
@@ -541,65 +499,22 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         fu = u;
         fst = st;
         enter();
-        Piece ahead;
-        fetch(ahead);
+        fetch();
         uint32_t slot = (uint32_t)grp, phase = 0;   // (the ring has more stages than there are groups)
         int unit = -1;
-        uint32_t nib[Piece::kPieces], negz[Piece::kPieces];   // kEpi: multiplier and bias of a row's pairs
         bool ok = true;
         while (u < p.n_units && ok) {
             if (unit != u) {
                 unit = u;
-                const int64_t n0 = (int64_t)(u / p.n_ttiles) * 2 * BM + rank * BM + r0;
-#pragma unroll
-                for (int j = 0; j < Piece::kPieces; ++j) {
-                    // a row whose s is 0 has weights 0, whatever its codes (the epilogue scales it by 1)
-                    const int64_t n = n0 + j * kRowStep;
-                    const bool live = n < p.Np && __ldg(p.s + n) != 0.0f;
-                    if constexpr (FORM == kQ8) {
-                        nib[j] = live ? 0x0F0F0F0Fu : 0u;
-                    } else {
-                        nib[j] = live ? 0x3F803F80u : 0u;
-                        negz[j] = live ? dequant_bias<false>(__ldg(p.z + n)) : 0u;
-                    }
-                }
+                d.set_rows(p.s, p.z, (int64_t)(u / p.n_ttiles) * 2 * BM + rank * BM, p.Np);
             }
-            // dequantise before the stage is free: 32 codes a piece, two (e4m3) or
-            // four (bf16) 16-byte pieces of the operand
-            constexpr int kOut = FORM == kQ8 ? 2 : 4;
-            uint4 o[Piece::kPieces][kOut];
-#pragma unroll
-            for (int j = 0; j < Piece::kPieces; ++j) {
-                const uint32_t words[4] = {ahead.w[j].x, ahead.w[j].y, ahead.w[j].z, ahead.w[j].w};
-                if constexpr (FORM == kQ8) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        nibbles_to_e4m3(words[2 * h], nib[j], o[j][h].x, o[j][h].y);
-                        nibbles_to_e4m3(words[2 * h + 1], nib[j], o[j][h].z, o[j][h].w);
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        o[j][h].x = dequant_pair_mul(words[h], nib[j], negz[j]);
-                        o[j][h].y = dequant_pair_mul(words[h] >> 4, nib[j], negz[j]);
-                        o[j][h].z = dequant_pair_mul(words[h] >> 8, nib[j], negz[j]);
-                        o[j][h].w = dequant_pair_mul(words[h] >> 12, nib[j], negz[j]);
-                    }
-                }
-            }
-            fetch(ahead);
+            // dequantise before the stage is free
+            d.convert();
+            fetch();
             // the stage is free once the MMAs of its last round are done
             ok = warp_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status);
             if (ok && st < p.n_main) {
-                uint8_t *const at = base_ptr + slot * STAGE_BYTES;
-#pragma unroll
-                for (int j = 0; j < Piece::kPieces; ++j) {
-                    const int row = r0 + j * kRowStep;
-#pragma unroll
-                    for (int h = 0; h < kOut; ++h)
-                        *reinterpret_cast<uint4 *>(at + row * ROW_BYTES + (((kOut * piece + h) ^ (row & 7)) << 4)) =
-                            o[j][h];
-                }
+                d.store(base_ptr + slot * STAGE_BYTES);
                 fence_proxy_async_smem();
                 __syncwarp();
             }
@@ -642,7 +557,7 @@ cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, 
                            unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
                            const float *rowc)
 {
-    const int BK = pair_bk(form);
+    const int BK = tc_stage_k(form);
     const uint64_t xd[2] = {(uint64_t)pk.K, (uint64_t)M};
     const uint64_t xst[1] = {(uint64_t)ldx * (uint64_t)(ROW_BYTES / BK)};
     const uint32_t xb[2] = {(uint32_t)BK, (uint32_t)(BN / 2)};

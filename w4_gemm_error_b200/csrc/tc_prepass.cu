@@ -101,6 +101,10 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    // the rows of G do not depend on earlier kernels: on their way to L2 now
+    if (mma && warp == 0)
+        for (int i = lane; i < nkb; i += 32)
+            tma_prefetch_2d(&tm_g, (rank + i * S) * 64, 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
