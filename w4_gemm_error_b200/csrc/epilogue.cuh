@@ -60,6 +60,9 @@ __device__ __forceinline__ float activate(float v, int act)
     }
 }
 
+// The same as a call, for code that runs once.
+static __device__ __noinline__ float activate_call(float v, int act) { return activate(v, act); }
+
 // Two fp32 values in one register pair, and the packed fp32 instructions of
 // sm_100 on them (each half rounded as the scalar instruction rounds it).
 using f32x2 = unsigned long long;

@@ -12,8 +12,8 @@
 // The tokens are the 128 rows (TMEM lanes) of the MMA and the rows of G its N.
 // One CTA a tile leaves most SMs idle (16 of them work at 2048 tokens, 29 us);
 // S = 8 there takes under a third of it.  e4m3 activations are made bf16 on
-// their way from the copied tile to the MMA's (exact), by the same four warps
-// that later read the accumulator, which sum X_t as they go.  The S partial
+// their way from the copied tile to the MMA's (exact), and sixteen rows of ones
+// behind those of G make X_t one more column of D.  The S partial
 // accumulators meet in shared memory: CTA q sums its 128 / S tokens over the
 // cluster in rank order (run-to-run identical), forms the gate and writes v.
 #include <algorithm>
@@ -27,14 +27,17 @@ namespace spear {
 namespace {
 
 constexpr int kTok = 128;
-constexpr int kStages = 4;
-constexpr int kThreads = 192;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxStages = 8;
+constexpr int kConvWarps = 8;      // warps 2-9: conversion (kQ8), then the accumulator (the first four)
+constexpr int kThreads = 64 + 32 * kConvWarps;
+constexpr int kMaxCluster = 16;
+constexpr int kOnesRows = 16;      // kQ8: rows of ones after those of G, whose product is X_t
 
 struct TcPrepass2Params {
     int64_t M;
     int n_k;              // 64-k blocks
     int S;                // CTAs a cluster
+    int stages;
     int R1p, r, rp;
     float b_g;
     const float *xs;      // kQ8
@@ -47,11 +50,18 @@ struct TcPrepass2Params {
 template <int FORM>
 __host__ __device__ constexpr uint32_t xin_bytes() { return FORM == kQ8 ? kTok * 64 : 0; }
 
-// Stage: the MMA's tile of x (16 KB), the copied e4m3 tile (kQ8), the rows of G.
+// Columns of D: the rows of G, then (kQ8) those of ones.
+template <int FORM>
+__host__ __device__ inline int columns(int R1p)
+{
+    return R1p + (FORM == kQ8 ? kOnesRows : 0);
+}
+// Stage: the MMA's tile of x (16 KB), the copied e4m3 tile (kQ8), the rows of G
+// (and of ones).
 template <int FORM>
 __host__ __device__ inline uint32_t stage_bytes(int R1p)
 {
-    return kTok * 128 + xin_bytes<FORM>() + (((uint32_t)R1p * 128 + 1023u) & ~1023u);
+    return kTok * 128 + xin_bytes<FORM>() + (((uint32_t)columns<FORM>(R1p) * 128 + 1023u) & ~1023u);
 }
 
 template <int FORM>
@@ -61,7 +71,7 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 {
     extern __shared__ uint8_t smem_raw[];
     // copied, staged (converted) and empty of each stage; accumulator done; drain
-    __shared__ __align__(8) uint64_t bars[3 * kStages + 2];
+    __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 2];
     __shared__ uint32_t tmem_base_slot;
     __shared__ volatile int abort_flag;
     __shared__ float s_gate[kTok];
@@ -69,25 +79,27 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t *const bp = smem_raw + (base - smem_addr(smem_raw));
-    const uint32_t full0 = smem_addr(&bars[0]), staged0 = smem_addr(&bars[kStages]);
-    const uint32_t empty0 = smem_addr(&bars[2 * kStages]);
-    const uint32_t done = smem_addr(&bars[3 * kStages]), drain = smem_addr(&bars[3 * kStages + 1]);
+    const uint32_t full0 = smem_addr(&bars[0]), staged0 = smem_addr(&bars[kMaxStages]);
+    const uint32_t empty0 = smem_addr(&bars[2 * kMaxStages]);
+    const uint32_t done = smem_addr(&bars[3 * kMaxStages]), drain = smem_addr(&bars[3 * kMaxStages + 1]);
     const uint32_t g_bytes = (uint32_t)p.R1p * 128, sbytes = stage_bytes<FORM>(p.R1p);
     constexpr uint32_t kXin = kTok * 128;                 // offset of the copied e4m3 tile
     const uint32_t o_g = kTok * 128 + xin_bytes<FORM>();  // offset of the rows of G
+    const int kStages = p.stages;
+    const int ncol = columns<FORM>(p.R1p);
     const int S = p.S, rank = S > 1 ? (int)cluster_ctarank() : 0;
     const int t0 = (int)(blockIdx.x / S) * kTok;
     const int nkb = (p.n_k - rank + S - 1) / S;   // this CTA's blocks (at least one)
-    const bool mma = p.R1p > 0;
+    const bool ec = p.R1p > 0;
     uint32_t tmem_cols = 32;
-    while (tmem_cols < (uint32_t)p.R1p)
+    while (tmem_cols < (uint32_t)ncol)
         tmem_cols <<= 1;
 
     if (tid == 0) {
         abort_flag = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(staged0 + 8 * s, 4);
+            mbar_init(staged0 + 8 * s, kConvWarps);
             mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(done, 1);
@@ -102,9 +114,18 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     // the rows of G do not depend on earlier kernels: on their way to L2 now
-    if (mma && warp == 0)
+    if (ec && warp == 0)
         for (int i = lane; i < nkb; i += 32)
             tma_prefetch_2d(&tm_g, (rank + i * S) * 64, 0);
+    if constexpr (FORM == kQ8) {
+        // the rows of ones of every stage, once (any order of a row will do)
+        for (int i = tid; i < kStages * kOnesRows * 8; i += kThreads) {
+            const int s = i / (kOnesRows * 8), e = i - s * (kOnesRows * 8);
+            *reinterpret_cast<uint4 *>(bp + s * sbytes + o_g + g_bytes + e * 16) =
+                make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        }
+        fence_proxy_async_smem();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -114,7 +135,6 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // and this CTA holds its tensor memory
     pdl_launch_dependents();
 
-    float xsum = 0.f;
     const int q = warp & 3, row = 32 * q + lane;   // warps 2-5: TMEM lane = token of the tile
     if (warp == 0) {
         if (lane == 0) {
@@ -127,7 +147,7 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 const int k = (rank + i * S) * 64;
                 mbar_expect_tx(full, (FORM == kQ8 ? xin_bytes<FORM>() : kTok * 128) + g_bytes);
                 tma_load_2d(FORM == kQ8 ? sb + kXin : sb, &tm_x, k, t0, full);
-                if (mma)
+                if (ec)
                     tma_load_2d(sb + o_g, &tm_g, k, 0, full);
             }
             if (abort_flag)
@@ -137,40 +157,51 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.R1p >> 3) << 17) |
-                                   ((uint32_t)(kTok >> 4) << 24);
-            bool ok = true;
-            for (int i = 0; i < nkb && ok; ++i) {
-                const uint32_t slot = i % kStages, phase = (i / kStages) & 1;
-                if (!mbar_wait((FORM == kQ8 ? staged0 : full0) + 8 * slot, phase, &abort_flag, p.status)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t sb = base + slot * sbytes;
-                const uint64_t a_desc = smem_desc_sw128(sb), b_desc = smem_desc_sw128(sb + o_g);
-                if (mma)
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, (i > 0 || k > 0) ? 1u : 0u);
+        const bool elected = elect_one();
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(ncol >> 3) << 17) |
+                               ((uint32_t)(kTok >> 4) << 24);
+        const uint64_t a0 = smem_desc_sw128(base), b0 = smem_desc_sw128(base + o_g);
+        uint32_t slot = 0, phase = 0;
+        bool ok = true;
+        for (int i = 0; i < nkb; ++i) {
+            if (!warp_wait((FORM == kQ8 ? staged0 : full0) + 8 * slot, phase, &abort_flag, p.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t a_desc = a0 + slot * (sbytes >> 4), b_desc = b0 + slot * (sbytes >> 4);
+            if (elected) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16(tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, (i > 0 || k > 0) ? 1u : 0u);
                 mma_commit(empty0 + 8 * slot);
             }
+            __syncwarp();
+            if ((int)++slot == kStages) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        if (elected) {
             if (ok)
                 mma_commit(done);
             mma_commit(drain);
-            mbar_wait_final(drain, 0);
         }
+        __syncwarp();
+        mbar_wait_final(drain, 0);
     } else if (FORM == kQ8) {
-        // e4m3 -> bf16: one token's 64 k a thread
+        // e4m3 -> bf16: half of one token's 64 k a thread
+        const int half = (warp - 2) >> 2;
+        uint32_t slot = 0, phase = 0;
         for (int i = 0; i < nkb; ++i) {
-            const uint32_t slot = i % kStages, phase = (i / kStages) & 1;
-            if (!mbar_wait(full0 + 8 * slot, phase, &abort_flag, p.status))
+            if (!warp_wait(full0 + 8 * slot, phase, &abort_flag, p.status))
                 break;
             uint8_t *const sb = bp + slot * sbytes;
             const uint8_t *src = sb + kXin + row * 64;
             uint8_t *dst = sb + row * 128;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c2 = 0; c2 < 2; ++c2) {
+                const int c = 2 * half + c2;
                 const uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ ((row >> 1) & 3)) << 4));
                 const uint32_t words[4] = {w.x, w.y, w.z, w.w};
                 uint32_t o[8];
@@ -179,9 +210,6 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     o[2 * h] = f16x2_to_bf16x2(e4m3x2_to_f16x2((uint16_t)words[h]));
                     o[2 * h + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2((uint16_t)(words[h] >> 16)));
                 }
-#pragma unroll
-                for (int h = 0; h < 8; ++h)
-                    xsum += bf16_lo(o[h]) + bf16_hi(o[h]);
                 *reinterpret_cast<uint4 *>(dst + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4 *>(dst + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
@@ -189,67 +217,82 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(staged0 + 8 * slot);
+            if ((int)++slot == kStages) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
     }
 
-    // ---- this CTA's partial: [token][R1p columns of D, X], odd row length (banks)
-    const int ld = p.R1p + 1;
+    // ---- this CTA's partial: [token][R1p columns of D, X], rows of whole 16 bytes
+    const int ld = p.R1p + 4;
+    const bool reader = warp >= 2 && warp < 6;
     float *const part = reinterpret_cast<float *>(bp);
-    const bool got = warp < 2 || mbar_wait(done, 0, &abort_flag, p.status);
+    const bool got = !reader || mbar_wait(done, 0, &abort_flag, p.status);
     __syncthreads();   // every copy and MMA of this CTA is over: the stages are free
-    if (warp >= 2) {
+    if (reader) {
         tc_fence_after();
         __syncwarp();
-        for (int c = 0; c < p.R1p; c += 16) {
+        for (int c = 0; c < ncol; c += 16) {
             uint32_t a[16];
             tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * q) << 16) + c, a);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                part[row * ld + c + j] = got ? __uint_as_float(a[j]) : 0.f;
+            for (int j = 0; j < 16; j += 4)
+                if (c + j < ld)   // (a few columns of the ones)
+                    *reinterpret_cast<float4 *>(part + row * ld + c + j) =
+                        got ? make_float4(__uint_as_float(a[j]), __uint_as_float(a[j + 1]), __uint_as_float(a[j + 2]),
+                                          __uint_as_float(a[j + 3]))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        part[row * ld + p.R1p] = xsum;
     }
     if (S > 1)
         cluster_sync();
     else
         __syncthreads();
 
-    // ---- the cluster's sums of this CTA's tokens
-    const int per = kTok / S, first = rank * per;
-    auto total = [&](int tt, int j) {
-        if (S == 1)
-            return part[(first + tt) * ld + j];
-        const uint32_t a = base + (uint32_t)(((first + tt) * ld + j) * 4);
-        float v[kMaxCluster];
+    // ---- the cluster's sums of this CTA's tokens, four columns a thread, in rank order
+    const int per = kTok / S, first = rank * per, nv = ld / 4;
+    const float *sums = part + first * ld;   // [per][ld]
+    if (S > 1) {
+        float *const own = part + kTok * ld;
+        for (int i = tid; i < per * nv; i += kThreads) {
+            const uint32_t a = base + (uint32_t)(first * ld + 4 * i) * 4;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s0 = 0; s0 < S; s0 += 8) {   // (eight loads in flight; S is a power of two)
+                float4 v[8];
 #pragma unroll
-        for (int s = 0; s < kMaxCluster; ++s)
-            v[s] = s < S ? ld_dsmem_f32(map_to_rank(a, (uint32_t)s)) : 0.f;
-        float sum = v[0];
+                for (int s = 0; s < 8; ++s)
+                    v[s] = s0 + s < S ? ld_dsmem_f4(map_to_rank(a, (uint32_t)(s0 + s))) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int s = 1; s < kMaxCluster; ++s)
-            if (s < S)
-                sum += v[s];
-        return sum;
-    };
+                for (int s = 0; s < 8; ++s) {
+                    sum.x += v[s].x;
+                    sum.y += v[s].y;
+                    sum.z += v[s].z;
+                    sum.w += v[s].w;
+                }
+            }
+            reinterpret_cast<float4 *>(own)[i] = sum;
+        }
+        sums = own;
+        __syncthreads();
+    }
     if (tid < per && t0 + first + tid < p.M) {
         const int64_t t = t0 + first + tid;
         float xs = 1.f;
         if constexpr (FORM == kQ8) {
             xs = __ldg(p.xs + t);
             p.rowc[rowc_at(t)] = 512.0f * xs;
-            p.rowc[rowc_at(t) + 2] = total(tid, p.R1p) * (1.0f / 512.0f);
+            p.rowc[rowc_at(t) + 2] = sums[tid * ld + p.R1p] * (1.0f / 512.0f);
         }
-        if (mma)
-            s_gate[tid] = 1.0f / (1.0f + expf(-(xs * total(tid, 0) + p.b_g))) * (FORM == kQ8 ? 1.0f / 512.0f : 1.0f);
+        if (ec)
+            s_gate[tid] = 1.0f / (1.0f + expf(-(xs * sums[tid * ld] + p.b_g))) * (FORM == kQ8 ? 1.0f / 512.0f : 1.0f);
     }
     __syncthreads();
-    if (mma)
-        for (int e = tid; e < per * p.rp; e += kThreads) {
-            const int tt = e / p.rp, j = e - tt * p.rp;
-            const int64_t t = t0 + first + tt;
-            if (t < p.M)
-                p.v[t * p.rp + j] = j < p.r ? to_tf32(s_gate[tt] * total(tt, 1 + j)) : 0.f;
-        }
+    if (ec)
+        for (int tt = warp; tt < per && t0 + first + tt < p.M; tt += kThreads / 32)
+            for (int j = lane; j < p.rp; j += 32)
+                p.v[(int64_t)(t0 + first + tt) * p.rp + j] =
+                    j < p.r ? to_tf32(s_gate[tt] * sums[tt * ld + 1 + j]) : 0.f;
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && p.ready)
@@ -290,18 +333,24 @@ cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, con
     p.status = status;
     p.ready = ready;
     const int64_t tiles = (M + kTok - 1) / kTok;
+    // as many CTAs as keep one SM each; a cluster of 16 (beyond the portable 8)
+    // only for blocks enough to be worth its longer exchange
     int S = 1;
-    while (S < kMaxCluster && 2 * S <= p.n_k && tiles * 2 * S <= num_sms)
+    while (S < kMaxCluster && 2 * S <= p.n_k && tiles * 2 * S <= num_sms && (S < 8 || p.n_k >= 8 * 2 * S))
         S *= 2;
     p.S = S;
     if (expected)
         *expected = (unsigned)(tiles * S);
-    const size_t ring = (size_t)kStages * (q8 ? stage_bytes<kQ8>(p.R1p) : stage_bytes<kEpi>(p.R1p));
-    const size_t part = (size_t)kTok * (p.R1p + 1) * sizeof(float);
+    const size_t stage = q8 ? stage_bytes<kQ8>(p.R1p) : stage_bytes<kEpi>(p.R1p);
+    p.stages = (int)std::min<size_t>(kMaxStages, 220 * 1024 / stage);
+    const size_t ring = p.stages * stage;
+    const size_t part = (size_t)(kTok + kTok / S) * (p.R1p + 4) * sizeof(float);   // partials, then sums
     const size_t smem = std::max(ring, part) + 1024;
     using Fn = void (*)(CUtensorMap, CUtensorMap, TcPrepass2Params);
     const Fn fn = q8 ? tc_prepass2_kernel<kQ8> : tc_prepass2_kernel<kEpi>;
     e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
+    if (e == cudaSuccess && S > 8)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

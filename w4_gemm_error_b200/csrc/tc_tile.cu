@@ -75,7 +75,7 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     uint8_t *const bp = smem_raw + (base - smem_addr(smem_raw));
     const uint32_t ready0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[STAGES]);
     const uint32_t done = smem_addr(&bars[2 * STAGES]), drain = smem_addr(&bars[2 * STAGES + 1]);
-    const int S = p.S, rank = S > 1 ? (int)cluster_ctarank() : 0, unit = (int)blockIdx.x / S;
+    const int S = p.S, rank = (int)cluster_ctarank(), unit = (int)blockIdx.x / S;
     const int t0 = (unit % p.n_ttiles) * BN, n0 = (unit / p.n_ttiles) * BM;
     const int lo = rank * p.n_main / S, nm = (rank + 1) * p.n_main / S - lo;   // (S <= n_main: at least one)
     const int nst = nm + (rank == S - 1 ? p.n_ec : 0);
@@ -307,67 +307,60 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         if (tid < BN / S && t0 + first + tid < p.M) {
             float x = 0.f;
             for (int s = 0; s < S; ++s)
-                x += S > 1 ? ld_dsmem_f32(map_to_rank(base + (uint32_t)(BN * BM + first + tid) * 4, (uint32_t)s))
-                           : part[BN * BM + first + tid];
+                x += ld_dsmem_f32(map_to_rank(base + (uint32_t)(BN * BM + first + tid) * 4, (uint32_t)s));
             s_const[tid] = make_float2(512.0f * __ldg(p.epi.xs + t0 + first + tid), x * (1.0f / 512.0f));
         }
         __syncthreads();
     }
     const int ntok = (int)max((int64_t)0, min((int64_t)(BN / S), p.M - t0 - first));
-    constexpr int kBatch = 4;   // pairs of outputs whose operands are in flight together
-    for (int i0 = tid; i0 < ntok * (BM / 2); i0 += kBatch * THREADS) {
-        uint32_t m[kBatch], r[kBatch];
-        float2 acc[kBatch];
-        bool on[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * THREADS, n = n0 + 2 * (i & (BM / 2 - 1));
-            const int64_t at = (int64_t)(t0 + first + i / (BM / 2)) * p.N + n;
-            on[b] = i < ntok * (BM / 2) && n < p.N;
-            m[b] = on[b] && p.epi.mul ? *reinterpret_cast<const uint32_t *>(p.epi.mul + at) : 0x3F803F80u;
-            r[b] = on[b] && p.epi.residual ? *reinterpret_cast<const uint32_t *>(p.epi.residual + at) : 0u;
+    // A thread's channels are the same for all its tokens (THREADS is a multiple
+    // of BM / 2).  This code runs once per CTA, from a cold instruction cache, so
+    // it is kept short: the loop is not unrolled and the activations are one
+    // function (unrolled by four with them inlined, this phase took 10000 cycles).
+    const int cp = tid & (BM / 2 - 1), n = n0 + 2 * cp;
+    if (n < p.N) {
+        const float2 sn = __ldg(reinterpret_cast<const float2 *>(p.s + n));
+        const float e0 = sn.x != 0.f ? sn.x : 1.f, e1 = sn.y != 0.f ? sn.y : 1.f;   // (B^T was divided by it)
+        float z0 = 0.f, z1 = 0.f;
+        if (FORM == kQ8) {
+            const uint32_t z = __ldg(reinterpret_cast<const uint16_t *>(p.z + n));
+            z0 = sn.x != 0.f ? (float)(z & 255u) : 0.f;
+            z1 = sn.y != 0.f ? (float)(z >> 8) : 0.f;
         }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int i = i0 + b * THREADS;
-            const uint32_t a = base + (uint32_t)((first + i / (BM / 2)) * BM + 2 * (i & (BM / 2 - 1))) * 4;
+        const uint32_t bias = p.epi.bias ? __ldg(reinterpret_cast<const uint32_t *>(p.epi.bias + n)) : 0u;
+#pragma unroll 1
+        for (int tt = tid / (BM / 2); tt < ntok; tt += THREADS / (BM / 2)) {
+            const int64_t at = (int64_t)(t0 + first + tt) * p.N + n;
+            const uint32_t m = p.epi.mul ? *reinterpret_cast<const uint32_t *>(p.epi.mul + at) : 0x3F803F80u;
+            const uint32_t r = p.epi.residual ? *reinterpret_cast<const uint32_t *>(p.epi.residual + at) : 0u;
+            const uint32_t a = base + (uint32_t)((first + tt) * BM + 2 * cp) * 4;
             float2 v[kMaxSplit];
 #pragma unroll
-            for (int s = 0; s < kMaxSplit; ++s)
-                if (s < S)
-                    v[s] = !on[b] ? make_float2(0.f, 0.f)
-                                  : (S > 1 ? ld_dsmem_f2(map_to_rank(a, (uint32_t)s))
-                                           : *reinterpret_cast<const float2 *>(bp + (a - base)));
-            acc[b] = v[0];
+            for (int s = 0; s < kMaxSplit; ++s)   // (all S loads in flight; a cluster of one reads itself)
+                v[s] = s < S ? ld_dsmem_f2(map_to_rank(a, (uint32_t)s)) : make_float2(0.f, 0.f);
+            float v0 = v[0].x, v1 = v[0].y;
 #pragma unroll
-            for (int s = 1; s < kMaxSplit; ++s)
-                if (s < S) {
-                    acc[b].x += v[s].x;
-                    acc[b].y += v[s].y;
-                }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            if (!on[b])
-                continue;
-            const int i = i0 + b * THREADS, n = n0 + 2 * (i & (BM / 2 - 1));
-            const int64_t t = t0 + first + i / (BM / 2);
-            const float2 sn = __ldg(reinterpret_cast<const float2 *>(p.s + n));
-            const float e0 = sn.x != 0.f ? sn.x : 1.f, e1 = sn.y != 0.f ? sn.y : 1.f;   // (B^T was divided by it)
-            float v0 = acc[b].x, v1 = acc[b].y;
+            for (int s = 1; s < kMaxSplit; ++s) {
+                v0 += v[s].x;
+                v1 += v[s].y;
+            }
             if constexpr (FORM == kQ8) {
-                const float cx = s_const[i / (BM / 2)].x, cy = s_const[i / (BM / 2)].y;
-                const float z0 = sn.x != 0.f ? (float)__ldg(p.z + n) : 0.f, z1 = sn.y != 0.f ? (float)__ldg(p.z + n + 1) : 0.f;
-                v0 = e0 * cx * (v0 - z0 * cy);
-                v1 = e1 * cx * (v1 - z1 * cy);
+                const float2 c = s_const[tt];
+                v0 = e0 * c.x * (v0 - z0 * c.y);
+                v1 = e1 * c.x * (v1 - z1 * c.y);
             } else {
                 v0 *= e0;
                 v1 *= e1;
             }
-            const uint32_t bias = p.epi.bias ? __ldg(reinterpret_cast<const uint32_t *>(p.epi.bias + n)) : 0u;
-            v0 = activate(v0 + bf16_lo(bias), p.epi.act) * bf16_lo(m[b]) + bf16_lo(r[b]);
-            v1 = activate(v1 + bf16_hi(bias), p.epi.act) * bf16_hi(m[b]) + bf16_hi(r[b]);
-            *reinterpret_cast<uint32_t *>(p.y + t * p.N + n) = pack_bf16x2(v0, v1);
+            v0 += bf16_lo(bias);
+            v1 += bf16_hi(bias);
+            if (p.epi.act != kActNone) {
+                v0 = activate_call(v0, p.epi.act);
+                v1 = activate_call(v1, p.epi.act);
+            }
+            v0 = v0 * bf16_lo(m) + bf16_lo(r);
+            v1 = v1 * bf16_hi(m) + bf16_hi(r);
+            *reinterpret_cast<uint32_t *>(p.y + at) = pack_bf16x2(v0, v1);
         }
     }
     if (S > 1)
