@@ -41,6 +41,7 @@ cudaError_t launch_prepass_q8(const Packed &pk, const void *xq, int64_t ldx, con
 cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, const float *xs, int64_t M, bool ec,
                                float *v, float *rowc, int form, const CUtensorMap *g, int *status, cudaStream_t st,
                                int num_sms, unsigned *ready, unsigned *expected);
+int tc_prepass2_split(const Packed &pk, int64_t M, int num_sms);   // its CTAs per 128 tokens
 const CUtensorMap *tc_map_g(const TcWork &w);   // (of a packed layer with an EC)
 
 bool tc_available(const Packed &pk);

@@ -30,7 +30,7 @@ constexpr int kTok = 128;
 constexpr int kMaxStages = 8;
 constexpr int kConvWarps = 8;      // warps 2-9: conversion (kQ8), then the accumulator (the first four)
 constexpr int kThreads = 64 + 32 * kConvWarps;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 constexpr int kOnesRows = 16;      // kQ8: rows of ones after those of G, whose product is X_t
 
 struct TcPrepass2Params {
@@ -251,11 +251,13 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         __syncthreads();
 
     // ---- the cluster's sums of this CTA's tokens, four columns a thread, in rank order
-    const int per = kTok / S, first = rank * per, nv = ld / 4;
-    const float *sums = part + first * ld;   // [per][ld]
+    // (the tile's real tokens, shared out evenly)
+    const int ntok = (int)min((int64_t)kTok, p.M - t0), per = (ntok + S - 1) / S;
+    const int first = min(rank * per, ntok), mine = min(per, ntok - first), nv = ld / 4;
+    const float *sums = part + first * ld;   // [mine][ld]
     if (S > 1) {
         float *const own = part + kTok * ld;
-        for (int i = tid; i < per * nv; i += kThreads) {
+        for (int i = tid; i < mine * nv; i += kThreads) {
             const uint32_t a = base + (uint32_t)(first * ld + 4 * i) * 4;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int s0 = 0; s0 < S; s0 += 8) {   // (eight loads in flight; S is a power of two)
@@ -276,7 +278,7 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         sums = own;
         __syncthreads();
     }
-    if (tid < per && t0 + first + tid < p.M) {
+    if (tid < mine) {
         const int64_t t = t0 + first + tid;
         float xs = 1.f;
         if constexpr (FORM == kQ8) {
@@ -289,7 +291,7 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     }
     __syncthreads();
     if (ec)
-        for (int tt = warp; tt < per && t0 + first + tt < p.M; tt += kThreads / 32)
+        for (int tt = warp; tt < mine; tt += kThreads / 32)
             for (int j = lane; j < p.rp; j += 32)
                 p.v[(int64_t)(t0 + first + tt) * p.rp + j] =
                     j < p.r ? to_tf32(s_gate[tt] * sums[tt * ld + 1 + j]) : 0.f;
@@ -306,6 +308,16 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 }
 
 }  // namespace
+
+// As many CTAs a tile as keep one SM each, up to the portable cluster of 8.
+int tc_prepass2_split(const Packed &pk, int64_t M, int num_sms)
+{
+    const int64_t tiles = (M + kTok - 1) / kTok;
+    int S = 1;
+    while (S < kMaxCluster && 2 * S <= (int)(pk.Kp / 64) && tiles * 2 * S <= num_sms)
+        S *= 2;
+    return S;
+}
 
 cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, const float *xs, int64_t M, bool ec,
                                float *v, float *rowc, int form, const CUtensorMap *g, int *status, cudaStream_t st,
@@ -333,24 +345,18 @@ cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, con
     p.status = status;
     p.ready = ready;
     const int64_t tiles = (M + kTok - 1) / kTok;
-    // as many CTAs as keep one SM each; a cluster of 16 (beyond the portable 8)
-    // only for blocks enough to be worth its longer exchange
-    int S = 1;
-    while (S < kMaxCluster && 2 * S <= p.n_k && tiles * 2 * S <= num_sms && (S < 8 || p.n_k >= 8 * 2 * S))
-        S *= 2;
+    const int S = tc_prepass2_split(pk, M, num_sms);
     p.S = S;
     if (expected)
         *expected = (unsigned)(tiles * S);
     const size_t stage = q8 ? stage_bytes<kQ8>(p.R1p) : stage_bytes<kEpi>(p.R1p);
     p.stages = (int)std::min<size_t>(kMaxStages, 220 * 1024 / stage);
     const size_t ring = p.stages * stage;
-    const size_t part = (size_t)(kTok + kTok / S) * (p.R1p + 4) * sizeof(float);   // partials, then sums
+    const size_t part = (size_t)(kTok + (kTok + S - 1) / S) * (p.R1p + 4) * sizeof(float);   // partials, then sums
     const size_t smem = std::max(ring, part) + 1024;
     using Fn = void (*)(CUtensorMap, CUtensorMap, TcPrepass2Params);
     const Fn fn = q8 ? tc_prepass2_kernel<kQ8> : tc_prepass2_kernel<kEpi>;
     e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
-    if (e == cudaSuccess && S > 8)
-        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -16,7 +16,7 @@
 // sum the codes of each token until then (mma.sync of the staged activations,
 // made f16, with a tile of ones: exact products), so that a layer without the
 // Error Compensator needs no prepass.
-// Then all of them take the outputs of the CTA's BN / S tokens, two channels a
+// Then all of them take the outputs of the CTA's 1/S of the tokens, two channels a
 // thread: the S partials, the epilogue, 4-byte stores of whole lines.
 // Every wait is bounded (about a second); one that runs out sets the handle's
 // status word and the kernel winds down.
@@ -301,10 +301,12 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(BN) : "memory");
     }
 
-    // ---- outputs: tokens rank * BN / S .., two channels a thread
-    const int first = rank * (BN / S);
+    // ---- outputs: this CTA's tokens, two channels a thread
+    // (the tile's real tokens, shared out evenly)
+    const int real = (int)min((int64_t)BN, p.M - t0), per = (real + S - 1) / S;
+    const int first = min(rank * per, real), ntok = min(per, real - first);
     if constexpr (FORM == kQ8) {
-        if (tid < BN / S && t0 + first + tid < p.M) {
+        if (tid < ntok) {
             float x = 0.f;
             for (int s = 0; s < S; ++s)
                 x += ld_dsmem_f32(map_to_rank(base + (uint32_t)(BN * BM + first + tid) * 4, (uint32_t)s));
@@ -312,7 +314,6 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         }
         __syncthreads();
     }
-    const int ntok = (int)max((int64_t)0, min((int64_t)(BN / S), p.M - t0 - first));
     // A thread's channels are the same for all its tokens (THREADS is a multiple
     // of BM / 2).  This code runs once per CTA, from a cold instruction cache, so
     // it is kept short: the loop is not unrolled and the activations are one
@@ -411,10 +412,20 @@ cudaError_t launch_tc_tile(const Packed &pk, const void *x, void *y, int64_t M, 
     p.rp = pk.rp;
     p.n_ttiles = (int)((M + BN - 1) / BN);
     const int64_t units = (int64_t)p.n_ttiles * (pk.Np / BM);
-    // K over as many CTAs as keep one SM each, at least four stages a CTA
-    int S = 1;
-    while (2 * S <= kMaxSplit && units * 2 * S <= num_sms && p.n_main >= 8 * S)
-        S *= 2;
+    const TileFn fn = form == kQ8 ? tile_fn<kQ8>(BN) : tile_fn<kEpi>(BN);
+    const int smem = tile_smem_bytes(BN);
+    e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
+    if (e != cudaSuccess)
+        return e;
+    // K over as many CTAs a tile as are all resident at once, at least four
+    // stages a CTA, beside the prepass with the EC (whose clusters of up to 8
+    // the count of whole clusters may not fit around: a quarter more; clusters
+    // that have to wait for it make the two run one after the other, 31 us
+    // instead of 24 at 64 tokens of a 14336x4096 layer)
+    const int64_t beside = use_ec ? (M + 127) / 128 * tc_prepass2_split(pk, M, num_sms) * 5 / 4 : 0;
+    int S = (int)std::min<int64_t>({kMaxSplit, std::max(1, p.n_main / 4), std::max<int64_t>(1, num_sms / units)});
+    while (S > 1 && !grid_is_one_wave(reinterpret_cast<const void *>(fn), THREADS, smem, S, units * S + beside, num_sms))
+        --S;
     p.S = S;
     p.codes = reinterpret_cast<const uint8_t *>(pk.codes);
     p.s = pk.s;
@@ -424,11 +435,6 @@ cudaError_t launch_tc_tile(const Packed &pk, const void *x, void *y, int64_t M, 
     p.v_ready = use_ec ? v_ready : nullptr;
     p.v_expected = v_expected;
     p.epi = epi;
-    const TileFn fn = form == kQ8 ? tile_fn<kQ8>(BN) : tile_fn<kEpi>(BN);
-    const int smem = tile_smem_bytes(BN);
-    e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
-    if (e != cudaSuccess)
-        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * S));
     cfg.blockDim = dim3(THREADS);
