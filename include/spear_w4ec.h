@@ -166,9 +166,10 @@ typedef struct spear_w4ec_epilogue {
  * spear_w4ec_forward's with SPEAR_FORCE_FUSED).  mul and residual may each be
  * y itself (in-place residual addition); every other overlap of y with an
  * operand is SPEAR_ERR_INVALID.  flags: as spear_w4ec_forward, except that the
- * EC is always formed in the kernel of the product: SPEAR_FORCE_SPLIT is
- * SPEAR_ERR_UNSUPPORTED, and a tuned table's path is followed without its
- * placement. */
+ * EC is always formed in the kernel of the product (SPEAR_FORCE_SPLIT is
+ * SPEAR_ERR_UNSUPPORTED) and the dispatch table, whose times are of the forward
+ * without an epilogue, is not used: without a path flag the decode kernels run
+ * up to 16 tokens and the tcgen05 kernels beyond. */
 int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M, const spear_w4ec_epilogue *ep,
                           uint32_t flags, void *stream);
 
@@ -178,8 +179,8 @@ int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M
  *   xs  dev float [M]: one scale a token
  * The products x (q - z) are exact and summed in fp32; a token with a NaN
  * code, or whose scale is not finite, has NaN or infinite outputs.  ep may be
- * NULL.  The dispatch table is not used: SPEAR_FORCE_DECODE and SPEAR_FORCE_TC
- * pick a kernel family as in spear_w4ec_forward. */
+ * NULL.  flags: as spear_w4ec_forward_ep (without a path flag the decode kernels
+ * run up to 8 tokens, up to 16 on layers of one CTA per 16 weight rows). */
 int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y, int64_t M,
                           const spear_w4ec_epilogue *ep, uint32_t flags, void *stream);
 

@@ -233,6 +233,42 @@ def test_calls_of_many_sizes_back_to_back(kind):
     assert lin.status() == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("M,K,N,r", [(64, 14336, 4096, 64), (64, 8192, 4096, 0), (33, 14336, 1024, 128),
+                                     (128, 4096, 4096, 32), (100, 2048, 14336, 16), (20, 4096, 4096, 128),
+                                     (300, 4096, 1000, 64), (700, 4096, 6144, 64), (16, 14336, 4096, 64),
+                                     (8, 14336, 4096, 64), (1, 4096, 14336, 64), (8, 4096, 4096, 32)])
+def test_many_calls_agree(kind, M, K, N, r):
+    """Calls of three layers in turn, nothing waited for between, all giving the same bits
+    and the right values: an operand overwritten while it is still read shows here."""
+    from w4_gemm_error_b200.spear import SPEAR_EC_OFF
+    lays = [LayerRef(K, N, r, seed=i, asym=i == 1) for i in range(3)]
+    lins = [lay.make(M) for lay in lays]
+    args = [(bf16_x(lay, M),) if kind == "bf16" else q8_x(lay, M) for lay in lays]
+    x = [a[0].double() if kind == "bf16" else a[0].double() * a[1].double()[:, None] for a in args]
+
+    def call(i, flags=0):
+        f = lins[i].forward_ep if kind == "bf16" else lins[i].forward_q8
+        return f(*args[i], act="relu", flags=flags)
+
+    first = [call(i) for i in range(3)]
+    for i in range(3):
+        assert_layer(first[i], lays[i], x[i], "first", act="relu")
+    off = [call(i, SPEAR_EC_OFF) for i in range(3)]
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for n in range(60):
+        i = n % 3
+        bad += (call(i) != first[i]).sum()
+        if n % 4 == 0:
+            bad += (call(i, SPEAR_EC_OFF) != off[i]).sum()
+    for n in range(30):
+        got = [call(i) for i in range(3)]    # back to back
+        for i in range(3):
+            bad += (got[i] != first[i]).sum()
+    assert bad.item() == 0
+    assert all(lin.status() == 0 for lin in lins)
+
+
 def test_results_repeat_bit_for_bit():
     lay = LayerRef(4096, 520, 64, seed=21)
     for M in (1, 16, 24, 64, 300):

@@ -20,7 +20,10 @@ def rows(M, K, seed=0, std=1.0):
 
 
 SHAPES = [(1, 8), (1, 4096), (3, 1), (2, 7), (5, 31), (4, 66), (37, 2050), (9, 2048), (2, 4104), (33, 1032),
-          (3, 14336), (2, 16384), (2, 16390), (1, 32768), (2, 40000), (1, 33001), (300, 256), (1, 131072)]
+          (3, 14336), (2, 16384), (2, 16390), (1, 32768), (2, 40000), (1, 33001), (300, 256), (1, 131072),
+          # many rows: the kernel that streams them, with one to four vectors a thread and one warp upwards
+          (700, 8), (1500, 64), (999, 264), (1201, 1032), (2049, 2048), (650, 4104), (800, 10000), (601, 14336),
+          (1200, 16384), (593, 2050)]
 
 
 @pytest.mark.parametrize("M,K", SHAPES)
@@ -57,10 +60,10 @@ def test_single_outputs_equal_the_joint_call():
     assert y2 is None and torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s)
 
 
-@pytest.mark.parametrize("K", [1032, 2050, 40000])
-def test_outputs_in_the_place_of_inputs(K):
+@pytest.mark.parametrize("M,K", [(7, 1032), (7, 2050), (7, 40000), (900, 1032), (700, 4096)])
+def test_outputs_in_the_place_of_inputs(M, K):
     from w4_gemm_error_b200.spear import rmsnorm
-    x, w, res = rows(7, K, 1), rows(1, K, 2)[0], rows(7, K, 3)
+    x, w, res = rows(M, K, 1), rows(1, K, 2)[0], rows(M, K, 3)
     y, _, _, h = rmsnorm(x, w, EPS, res)
     for sum_in, y_in in (("res", None), ("x", None), ("res", "x"), ("x", "res"), (None, "x"), (None, "res")):
         t = {"x": x.clone(), "res": res.clone(), None: None}
@@ -71,10 +74,10 @@ def test_outputs_in_the_place_of_inputs(K):
     assert torch.equal(y3, rmsnorm(x, w, EPS)[0])
 
 
-@pytest.mark.parametrize("K", [256, 1030, 40000])
-def test_zero_tiny_and_bad_rows(K):
+@pytest.mark.parametrize("M,K", [(8, 256), (8, 1030), (8, 40000), (800, 256), (700, 4104)])
+def test_zero_tiny_and_bad_rows(M, K):
     from w4_gemm_error_b200.spear import quantize_q8, rmsnorm
-    x = rows(8, K, 1)
+    x = rows(M, K, 1)
     x[1] = 0
     x[2] = 1e-36
     x[3] = 1e30
@@ -98,17 +101,18 @@ def test_zero_tiny_and_bad_rows(K):
     assert torch.isnan(y[5]).all() and torch.isnan(s[5])
 
 
-def test_rows_past_the_last_are_left_alone():
+@pytest.mark.parametrize("M", [5, 777])
+def test_rows_past_the_last_are_left_alone(M):
     from w4_gemm_error_b200.spear import rmsnorm
     K = 1032
     w = rows(1, K, 2)[0]
-    big = {n: torch.full((9, K), 7, dtype=torch.bfloat16, device="cuda") for n in ("y", "h")}
-    q = torch.full((9, K), 7, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
-    s = torch.full((9,), 7.0, device="cuda")
-    rmsnorm(rows(5, K, 1), w, EPS, rows(5, K, 3), q8=True, out=big["y"][:5], out_q=q[:5], out_s=s[:5],
-            out_sum=big["h"][:5])
-    assert (big["y"][5:] == 7).all() and (big["h"][5:] == 7).all() and (s[5:] == 7).all()
-    assert (q.view(torch.uint8)[5:] == 7).all()
+    big = {n: torch.full((M + 4, K), 7, dtype=torch.bfloat16, device="cuda") for n in ("y", "h")}
+    q = torch.full((M + 4, K), 7, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s = torch.full((M + 4,), 7.0, device="cuda")
+    rmsnorm(rows(M, K, 1), w, EPS, rows(M, K, 3), q8=True, out=big["y"][:M], out_q=q[:M], out_s=s[:M],
+            out_sum=big["h"][:M])
+    assert (big["y"][M:] == 7).all() and (big["h"][M:] == 7).all() and (s[M:] == 7).all()
+    assert (q.view(torch.uint8)[M:] == 7).all()
 
 
 def test_offsets_past_32_bits():

@@ -136,6 +136,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// Before a warp arrives on a barrier that lets the next copy overwrite what it
+// has read: `seen` is made from every lane's loads.  The arithmetic on the
+// loaded values may be scheduled after the arrival, so that nothing else waits
+// for them; a branch on them does (without it, sums came out wrong).
+__device__ __forceinline__ void loads_complete(uint32_t seen)
+{
+    if (__all_sync(0xffffffffu, seen == 0x9E3779B9u))
+        __nanosleep(0);
+}
+
 // A warp's wait: every lane waits, all learn the same outcome.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status)
 {

@@ -28,7 +28,7 @@ struct spear_w4ec {
     PrepassWork pre{};
     DecodeWork dec{};
     TcWork tc{};
-    spear::PrepassQ8Work preq8{};
+    float *rowc = nullptr;      // per-token constants of the 8-bit forward (rowc_at)
     int *status = nullptr;      // sticky device status bits
     unsigned *vready = nullptr; // prepass -> tcgen05 kernel: [0] counts of v written, [1] CTAs done
     // staging for forward_host

@@ -68,7 +68,7 @@ void free_all(spear_w4ec *h)
     cudaFree(h->x_stage);
     cudaFree(h->y_stage);
     cudaFree(h->xq_pad);
-    prepass_q8_free(h->preq8);
+    cudaFree(h->rowc);
 }
 
 int from_cuda(cudaError_t e)
@@ -93,6 +93,27 @@ uint32_t default_path(const spear_w4ec *h, int64_t M)
 {
     const bool dec = decode_supported(h->pk, h->num_sms);
     if (!tc_supported(h) || (dec && M <= kDecodeMaxTokens))
+        return SPEAR_FORCE_DECODE;
+    return SPEAR_FORCE_TC;
+}
+
+// Path of the forms kEpi and kQ8 (the table's times are of the plain kernels,
+// whose tcgen05 family is another one).  Measured in us per call, chained,
+// decode against tcgen05 (bf16 / 8 bits):
+//   4096 x 4096, r 32 (row-CTA kernel)   16 tokens  8.1 / 10.3 against 13.1 / 12.3
+//                                        24 tokens 19.0 / 18.6 against 13.1 / 12.4
+//   4096 x 14336, r 64 (split-K kernel)   8 tokens 14.9 / 16.3 against 22.5 / 18.6
+//                                        16 tokens 20.2 / 21.1 against 23.0 / 19.1
+//                                        24 tokens 31.2 / 32.8 against 23.2 / 19.4
+//   14336 x 4096, r 64 (split-K kernel)  16 tokens 23.5 / 24.0 against 26.6 / 22.3
+// so: the decode kernels up to 16 tokens, but with 8 bits only up to 8 where
+// the row-CTA kernel does not run.
+uint32_t form_path(const spear_w4ec *h, int64_t M, int form)
+{
+    int64_t most = 16;
+    if (form == kQ8 && M > 8 && M <= 16 && !decode_rows_fits(h->pk, M, h->num_sms, form))
+        most = 8;
+    if (!tc_supported(h) || (M <= most && decode_supported(h->pk, h->num_sms)))
         return SPEAR_FORCE_DECODE;
     return SPEAR_FORCE_TC;
 }
@@ -142,17 +163,51 @@ Epilogue epi_rows(Epilogue e, int64_t t0, int64_t N)
     return e;
 }
 
+// The forms kEpi and kQ8 of the forward pass on the tcgen05 kernels, rows of x
+// ldx elements apart.  As in run_forward, with the EC the product's main stages
+// start beside the prepass, which counts what it has written into vready.
+int run_tc_form(const spear_w4ec *h, const void *x, int64_t ldx, void *y, int64_t M, bool ec, cudaStream_t st, int form,
+                const Epilogue &epi)
+{
+    const Packed &pk = h->pk;
+    if (h->fault_timeout) {
+        // injected fault: report what a wait that ran out reports, launch nothing
+        const int bits = kStatusTimeout;
+        return from_cuda(cudaMemcpyAsync(h->status, &bits, sizeof(int), cudaMemcpyHostToDevice, st));
+    }
+    const bool pair = tc_use_pair(pk, M, h->num_sms);
+    unsigned *ready = ec ? h->vready : nullptr;
+    unsigned expected = 0;
+    cudaError_t e = cudaSuccess;
+    // (without the EC only the pair kernel's 8-bit form needs one)
+    if (ec || (pair && form == kQ8))
+        e = launch_tc_prepass2(pk, x, ldx, epi.xs, M, ec, h->v, h->rowc, form, tc_map_g(h->tc), h->status, st,
+                               h->num_sms, ready, &expected);
+    if (e != cudaSuccess)
+        return from_cuda(e);
+    e = pair ? launch_tc_pair(pk, x, y, M, h->v, ec, tc_map_bt(h->tc), h->status, st, h->num_sms, ready, expected, form,
+                              epi, ldx, h->rowc)
+             : launch_tc_tile(pk, x, y, M, h->v, ec, tc_map_bt(h->tc), h->status, st, h->num_sms, ready, expected, form,
+                              epi, ldx);
+    if (e != cudaSuccess && ready)
+        cudaMemsetAsync(h->vready, 0, 2 * sizeof(unsigned), st);   // nothing will reset the prepass's counts
+    return from_cuda(e);
+}
+
 // form and epi: see epilogue.cuh.  The forms with an epilogue form the EC in
-// the same kernel as the product, whatever placement the table holds: y is
-// written once, after its last operand was read.
+// the same kernel as the product: y is written once, after its last operand was
+// read.
 int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t flags, cudaStream_t st,
                 int form = kPlain, const Epilogue &epi = Epilogue())
 {
     const Packed &pk = h->pk;
     const bool ec = pk.r > 0 && !(flags & SPEAR_EC_OFF);
     uint32_t choice = resolve(h, M, flags);
-    if (form != kPlain && !(flags & SPEAR_FORCE_SPLIT))
-        choice = (choice & ~(uint32_t)SPEAR_FORCE_SPLIT) | SPEAR_FORCE_FUSED;
+    if (form != kPlain) {
+        const uint32_t path = flags & (SPEAR_FORCE_DECODE | SPEAR_FORCE_TC);
+        const uint32_t mode = flags & (SPEAR_FORCE_FUSED | SPEAR_FORCE_SPLIT);
+        choice = (path ? path : form_path(h, M, form)) | (mode ? mode : (uint32_t)SPEAR_FORCE_FUSED);
+    }
     if ((choice & SPEAR_FORCE_DECODE) && (choice & SPEAR_FORCE_TC))
         return SPEAR_ERR_INVALID;
     if ((choice & SPEAR_FORCE_FUSED) && (choice & SPEAR_FORCE_SPLIT))
@@ -162,6 +217,8 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
         return SPEAR_ERR_UNSUPPORTED;
     if (h->fault_launch)
         return SPEAR_ERR_CUDA;
+    if (form != kPlain && (choice & SPEAR_FORCE_TC))
+        return tc_supported(h) ? run_tc_form(h, x, pk.K, y, M, ec, st, form, epi) : SPEAR_ERR_UNSUPPORTED;
     cudaError_t e = cudaSuccess;
     const bool decode = (choice & SPEAR_FORCE_DECODE) != 0;
     if (decode && !decode_supported(pk, h->num_sms))
@@ -172,12 +229,8 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
     const bool early = ec && fused && (choice & SPEAR_FORCE_TC) && tc_supported(h);
     unsigned expected = 0;
     if (ec && !(decode && fused)) {
-        if (form == kEpi && (choice & SPEAR_FORCE_TC))
-            e = launch_tc_prepass2(pk, x, pk.K, nullptr, M, true, h->v, nullptr, kEpi, tc_map_g(h->tc), h->status, st,
-                                   h->num_sms, early ? h->vready : nullptr, &expected);
-        else
-            e = run_prepass(h, x, M, (choice & SPEAR_FORCE_TC) != 0 && fused, st, early ? h->vready : nullptr,
-                            &expected);
+        e = run_prepass(h, x, M, (choice & SPEAR_FORCE_TC) != 0 && fused, st, early ? h->vready : nullptr,
+                        &expected);
         if (e != cudaSuccess)
             return from_cuda(e);
     }
@@ -185,7 +238,7 @@ int run_forward(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t
         if (!tc_supported(h))
             return SPEAR_ERR_UNSUPPORTED;
         e = launch_tc(pk, x, y, M, h->v, ec && fused, h->tc, h->status, h->fault_timeout, st, h->num_sms,
-                      early ? h->vready : nullptr, expected, form, epi, pk.K, nullptr);
+                      early ? h->vready : nullptr, expected);
         if (e != cudaSuccess || (early && h->fault_timeout)) {
             // nothing will reset the prepass's counts: clear them for the next forward
             cudaMemsetAsync(h->vready, 0, 2 * sizeof(unsigned), st);
@@ -238,7 +291,7 @@ int run_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y
         return SPEAR_ERR_UNSUPPORTED;
     uint32_t path = flags & (SPEAR_FORCE_DECODE | SPEAR_FORCE_TC);
     if (!path)
-        path = default_path(h, M);
+        path = form_path(h, M, kQ8);
     if (!path_supported(h, path))
         return SPEAR_ERR_UNSUPPORTED;
     if (h->fault_launch)
@@ -264,24 +317,8 @@ int run_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y
         xq = h->xq_pad;
         ldx = pk.K + 8;
     }
-    if (path == SPEAR_FORCE_TC) {
-        // as in run_forward: with the EC the product's main stages start beside
-        // the prepass, which counts what it has written into vready
-        unsigned expected = 0;
-        unsigned *ready = ec ? h->vready : nullptr;
-        // (without the EC only the pair kernel needs one: the other sums the codes itself)
-        cudaError_t e = cudaSuccess;
-        if (ec || tc_use_pair(pk, M, h->num_sms))
-            e = launch_tc_prepass2(pk, xq, ldx, xs, M, ec, h->v, h->preq8.rowc, kQ8, tc_map_g(h->tc), h->status, st,
-                                   h->num_sms, ready, &expected);
-        if (e != cudaSuccess)
-            return from_cuda(e);
-        e = launch_tc(pk, xq, y, M, h->v, ec, h->tc, h->status, h->fault_timeout, st, h->num_sms,
-                      ready, expected, kQ8, epi, ldx, h->preq8.rowc);
-        if (e != cudaSuccess || (ec && h->fault_timeout))
-            cudaMemsetAsync(h->vready, 0, 2 * sizeof(unsigned), st);
-        return from_cuda(e);
-    }
+    if (path == SPEAR_FORCE_TC)
+        return run_tc_form(h, xq, ldx, y, M, ec, st, kQ8, epi);
     for (int64_t t0 = 0; t0 < M; t0 += kDecodeMaxTokens) {
         const int64_t m = std::min<int64_t>(kDecodeMaxTokens, M - t0);
         const cudaError_t e = launch_decode_form(pk, static_cast<const uint8_t *>(xq) + t0 * ldx, ldx,
@@ -467,7 +504,7 @@ int spear_w4ec_create(spear_w4ec **out, int64_t K, int64_t N, int32_t r, const s
     chk(tc_alloc(pk, h->max_M, h->num_sms, h->tc));
     chk(alloc_zero(&h->status, 1));
     chk(alloc_zero(&h->vready, 2));
-    chk(prepass_q8_alloc(pk, h->max_M, h->num_sms, h->preq8));
+    chk(alloc_zero(&h->rowc, rowc_floats(h->max_M)));
     if (K % 16)
         chk(alloc_zero(&h->xq_pad, (size_t)h->max_M * (size_t)(K + 8)));
     if (e == cudaSuccess)

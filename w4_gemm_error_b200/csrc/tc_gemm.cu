@@ -42,7 +42,6 @@
 #include <new>
 
 #include "async_utils.cuh"
-#include "epilogue.cuh"
 #include "tc_gemm.h"
 #include "tensor_map.h"
 
@@ -50,30 +49,19 @@ namespace spear {
 namespace {
 
 constexpr int BM = 128;                       // weight rows per tile (TMEM lanes)
-constexpr int ROW_BYTES = 128;                // one swizzle atom: a stage's k of one row of either operand
-// k per stage: 64 bf16 or (form kQ8) 128 e4m3 values
-__host__ __device__ constexpr int tc_bk(int form) { return form == kQ8 ? 128 : 64; }
-constexpr int A_BYTES = BM * ROW_BYTES;       // 16 KB dequantised weights (or B^T on EC stages)
-__host__ __device__ constexpr int tc_c_bytes(int form) { return BM * tc_bk(form) / 2; }   // int4 codes
+constexpr int BK = 64;                        // k per stage: one 128-byte swizzle atom of bf16
+constexpr int A_BYTES = BM * BK * 2;          // 16 KB dequantised weights (or B^T on EC stages)
+constexpr int C_BYTES = BM * BK / 2;          // 4 KB int4 codes
 constexpr int THREADS = 704;   // 22 warps: TMA, MMA, 2 x 8 dequantisers, 4 epilogue
 
 // Token tile BN (the MMA N: 32, 64, 128 or 256) and what depends on it: the
-// activation tile of a stage (BN rows, or v on EC stages), the ring depth
-// (more stages for narrower tiles, within about 225 KB) and two accumulators of
+// activation tile of a stage (BN x 64 bf16, or v on EC stages), the ring depth
+// (more stages for narrower tiles, within about 210 KB) and two accumulators of
 // BN columns in TMEM.
-__host__ __device__ constexpr int tc_b_bytes(int BN) { return BN * ROW_BYTES; }
-__host__ __device__ constexpr int tc_stage_bytes(int BN, int form)
-{
-    return A_BYTES + tc_b_bytes(BN) + tc_c_bytes(form);
-}
-__host__ __device__ constexpr int tc_stages(int BN, int form)
-{
-    return BN >= 256 ? 4 : (BN >= 128 ? (form == kQ8 ? 5 : 6) : (BN >= 64 ? 7 : 8));
-}
-__host__ __device__ constexpr int tc_smem_bytes(int BN, int form)
-{
-    return tc_stages(BN, form) * tc_stage_bytes(BN, form) + 1024;
-}
+__host__ __device__ constexpr int tc_b_bytes(int BN) { return BN * BK * 2; }
+__host__ __device__ constexpr int tc_stage_bytes(int BN) { return A_BYTES + tc_b_bytes(BN) + C_BYTES; }
+__host__ __device__ constexpr int tc_stages(int BN) { return BN >= 256 ? 4 : (BN >= 128 ? 6 : (BN >= 64 ? 7 : 8)); }
+__host__ __device__ constexpr int tc_smem_bytes(int BN) { return tc_stages(BN) * tc_stage_bytes(BN) + 1024; }
 
 struct TcParams {
     int64_t M, N;
@@ -98,13 +86,10 @@ struct TcParams {
     // kernel waits for its predecessor first, as usual.
     unsigned *v_ready;
     unsigned v_expected;
-    Epilogue epi;          // forms kEpi and kQ8
-    const float *rowc;     // form kQ8: 2^9 xs[t] and 2^-9 sum_k xq[t,k] from the prepass (rowc_at)
 };
 
 struct Maps {
     CUtensorMap codes;
-    CUtensorMap codes128;   // the same codes in boxes of 128 k x 64 rows, 64B swizzle (form kQ8)
     CUtensorMap bt;
     CUtensorMap g;   // G = [w_g; A^T] [R1p][Kp] bf16, boxes of 64 x R1p, 128B swizzle
 };
@@ -268,57 +253,14 @@ tc_prepass_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 
 // ---------------------------------------------------------------- the kernel
 
-// Eight outputs of channel n, tokens t .. t + 7 below M: y = e_n * acc, through
-// the epilogue in form kEpi (its eight operand loads are issued before any is
-// used; they come after the accumulator is complete, and so after every kernel
-// that this one waits for).
-// Form kQ8: acc is 2^-9 sum_k xq q (the codes q themselves are the e4m3 bit
-// patterns of 2^-9 q), so that Y = xs e_n (2^9 acc - z sum_k xq).
-template <int FORM>
-__device__ __forceinline__ void store_outputs8(const TcParams &p, int64_t t, int64_t n, float e_n, float z_n,
-                                               float bias, const float (&acc)[8])
-{
-    EpiOperands eo[FORM == kPlain ? 1 : 8];
-    float2 rc[FORM == kQ8 ? 8 : 1];
-    if constexpr (FORM != kPlain) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if constexpr (FORM == kQ8)
-                rc[j] = t + j < p.M ? make_float2(__ldcg(p.rowc + rowc_at(t + j)), __ldcg(p.rowc + rowc_at(t + j) + 2))
-                                    : make_float2(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            eo[j].bias = bias;
-            if (p.epi.mul && t + j < p.M)
-                eo[j].mul = bf16_lo(p.epi.mul[(t + j) * p.N + n]);
-            if (p.epi.residual && t + j < p.M)
-                eo[j].residual = bf16_lo(p.epi.residual[(t + j) * p.N + n]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (t + j >= p.M)
-            continue;
-        float v = e_n * acc[j];
-        if constexpr (FORM == kQ8)
-            v = e_n * rc[j].x * (acc[j] - z_n * rc[j].y);
-        if constexpr (FORM != kPlain)
-            v = epi_apply(p.epi, v, eo[j]);
-        p.y[(t + j) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    }
-}
-
-template <int BN, int FORM>
+template <int BN>
 __global__ void __launch_bounds__(THREADS, 1)
 tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_codes,
                const __grid_constant__ CUtensorMap tm_bt, const __grid_constant__ CUtensorMap tm_v, TcParams p)
 {
-    constexpr int BK = tc_bk(FORM);
-    constexpr int C_BYTES = tc_c_bytes(FORM);
-    constexpr int STAGES = tc_stages(BN, FORM);
+    constexpr int STAGES = tc_stages(BN);
     constexpr int B_BYTES = tc_b_bytes(BN);
-    constexpr int STAGE_BYTES = tc_stage_bytes(BN, FORM);
-    constexpr int SUB = 256 / BK;   // stages per tiled code block
+    constexpr int STAGE_BYTES = tc_stage_bytes(BN);
     constexpr int TMEM_COLS = 2 * BN;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[3 * STAGES + 5];
@@ -390,9 +332,9 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     if (st < p.n_main) {
                         mbar_expect_tx(full, B_BYTES + C_BYTES);
                         tma_load_2d(sb + A_BYTES, &tm_x, st * BK, t0, full);
-                        const int blk = (n0 / 64) * p.kchunks + st / SUB, sub = st % SUB;
-                        tma_load_4d(sb + A_BYTES + B_BYTES, &tm_codes, 0, sub, 0, blk, full);
-                        tma_load_4d(sb + A_BYTES + B_BYTES + C_BYTES / 2, &tm_codes, 0, sub, 0, blk + p.kchunks,
+                        const int blk = (n0 / 64) * p.kchunks + st / 4;
+                        tma_load_4d(sb + A_BYTES + B_BYTES, &tm_codes, 0, st & 3, 0, blk, full);
+                        tma_load_4d(sb + A_BYTES + B_BYTES + C_BYTES / 2, &tm_codes, 0, st & 3, 0, blk + p.kchunks,
                                     full);
                     } else {
                         if (!v_seen) {
@@ -435,9 +377,8 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         if (lane == 0) {
-            const uint32_t ab = FORM == kQ8 ? 0u : (1u << 7) | (1u << 10);   // A, B: e4m3 or bf16
             const uint32_t idesc = (1u << 4)                    // D: f32
-                                   | ab
+                                   | (1u << 7) | (1u << 10)     // A, B: bf16
                                    | ((uint32_t)(BN >> 3) << 17)
                                    | ((uint32_t)(BM >> 4) << 24);
             const uint32_t idesc_tf32 = (1u << 4)               // D: f32
@@ -472,14 +413,8 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     const uint32_t sb = base + slot * STAGE_BYTES;
                     const uint64_t a_desc = smem_desc_sw128(sb), b_desc = smem_desc_sw128(sb + A_BYTES);
                     if (st < p.n_main) {
-                        // 32 bytes of k an instruction
-                        for (int k = 0; k < ROW_BYTES / 32; ++k) {
-                            const uint32_t accumulate = (i > 0 || k > 0) ? 1u : 0u;
-                            if constexpr (FORM == kQ8)
-                                mma_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
-                            else
-                                mma_bf16(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
-                        }
+                        for (int k = 0; k < BK / 16; ++k)
+                            mma_bf16(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, (i > 0 || k > 0) ? 1u : 0u);
                     } else {
                         // EC: 32 tf32 values of j per 128-byte row, 8 per instruction
                         const int rem = p.rp - (st - p.n_main) * 32;
@@ -514,7 +449,6 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const uint32_t zb = __bfloat16_as_ushort(__float2bfloat16_rn(-(float)(128u + p.z[n])));
             const uint32_t negz = live ? (zb | (zb << 16)) : 0u;
             const uint32_t mulz = live ? 0x3F803F80u : 0u;
-            const uint32_t nib = live ? 0x0F0F0F0Fu : 0u;
             bool ok = true;
             for (int ii = 0; ii < nst; ++ii, ++g) {
                 if ((g & 1u) != grp)
@@ -525,26 +459,7 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     ok = false;
                     break;
                 }
-                if (FORM == kQ8 && st < p.n_main) {
-                    uint8_t *sb = base_ptr + slot * STAGE_BYTES;
-                    const uint8_t *crow = sb + A_BYTES + B_BYTES + i * 64;
-                    uint8_t *arow = sb + i * 128;
-                    // code row i: 64 bytes (128 k), its four 16-byte pieces permuted by
-                    // row bits 1 and 2 (64-byte TMA swizzle, conflict-free reads)
-#pragma unroll
-                    for (int c = 2 * half; c < 2 * half + 2; ++c) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(crow + ((c ^ ((i >> 1) & 3)) << 4));
-                        // 16 codes a store, eight a word: see nibbles_to_e4m3
-                        uint4 o;
-                        nibbles_to_e4m3(w.x, nib, o.x, o.y);
-                        nibbles_to_e4m3(w.y, nib, o.z, o.w);
-                        *reinterpret_cast<uint4 *>(arow + (((2 * c) ^ (i & 7)) << 4)) = o;
-                        nibbles_to_e4m3(w.z, nib, o.x, o.y);
-                        nibbles_to_e4m3(w.w, nib, o.z, o.w);
-                        *reinterpret_cast<uint4 *>(arow + (((2 * c + 1) ^ (i & 7)) << 4)) = o;
-                    }
-                    fence_proxy_async_smem();
-                } else if (st < p.n_main) {
+                if (st < p.n_main) {
                     uint8_t *sb = base_ptr + slot * STAGE_BYTES;
                     // code row i: 32 bytes (64 k), its two 16-byte halves swapped in rows
                     // with bit 2 set (32-byte TMA swizzle, conflict-free reads)
@@ -585,29 +500,6 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const int64_t n = (int64_t)(tile / p.n_ttiles) * BM + row;
             const float sn = p.s[n];
             const float e_n = sn != 0.0f ? sn : 1.0f;   // the EC operand was divided by it
-            const float bias = FORM != kPlain && p.epi.bias && n < p.N ? bf16_lo(__ldg(p.epi.bias + n)) : 0.f;
-            const float z_n = FORM == kQ8 && sn != 0.0f ? (float)p.z[n] : 0.f;
-            if (FORM != kPlain && p.ksplit == 1) {
-                // 16 columns at a time: the operands of eight outputs take the registers
-#pragma unroll 1
-                for (int c = 0; c < BN / 16; ++c) {
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * q) << 16) + buf * BN + 16 * c, r);
-                    if (n < p.N) {
-#pragma unroll
-                        for (int j0 = 0; j0 < 16; j0 += 8) {
-                            float a[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                a[j] = __uint_as_float(r[j0 + j]);
-                            store_outputs8<FORM>(p, t0 + 16 * c + j0, n, e_n, z_n, bias, a);
-                        }
-                    }
-                }
-                tc_fence_before();
-                mbar_arrive(tempty0 + 8 * buf);
-                continue;
-            }
             if (p.ksplit == 1) {
 #pragma unroll 1
                 for (int c = 0; c < BN / 32; ++c) {
@@ -615,12 +507,11 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(32 * q) << 16) + buf * BN + 32 * c, r);
                     if (n < p.N) {
 #pragma unroll
-                        for (int j0 = 0; j0 < 32; j0 += 8) {
-                            float a[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                a[j] = __uint_as_float(r[j0 + j]);
-                            store_outputs8<FORM>(p, t0 + 32 * c + j0, n, e_n, z_n, bias, a);
+                        for (int j = 0; j < 32; ++j) {
+                            const int64_t t = t0 + 32 * c + j;
+                            if (t < p.M)
+                                p.y[t * p.N + n] =
+                                    __bfloat16_as_ushort(__float2bfloat16_rn(e_n * __uint_as_float(r[j])));
                         }
                     }
                 }
@@ -667,8 +558,10 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                         for (int jj = 0; jj < 8; ++jj)
                             v[jj] += w[jj];
                     }
-                    if (n < p.N)
-                        store_outputs8<FORM>(p, t0 + j0, n, e_n, z_n, bias, v);
+#pragma unroll
+                    for (int jj = 0; jj < 8; ++jj)
+                        if (j0 + jj < jn && n < p.N)
+                            p.y[(t0 + j0 + jj) * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(e_n * v[jj]));
                 }
                 if (q == 0 && lane == 0)
                     p.counters[tile] = 0u;   // for the next forward
@@ -696,6 +589,7 @@ tc_w4ec_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 bool tc_available(const Packed &) { return tensor_maps_available(); }
 
 const CUtensorMap *tc_map_g(const TcWork &w) { return &static_cast<const Maps *>(w.maps)->g; }
+const CUtensorMap *tc_map_bt(const TcWork &w) { return &static_cast<const Maps *>(w.maps)->bt; }
 
 // Split K for narrow layers: up to 128 tokens, when the 128-row tiles fill at
 // most half of the SMs, K is split into as many parts as keep one unit per SM
@@ -751,13 +645,6 @@ cudaError_t tc_prepare(const Packed &pk, TcWork &w)
     const uint32_t box[4] = {8, 1, 64, 1};
     cudaError_t e = make_map_nd(&m->codes, pk.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, dims, strides, box,
                                 CU_TENSOR_MAP_SWIZZLE_32B);
-    if (e == cudaSuccess) {
-        const uint64_t dims2[4] = {16, 2, 64, dims[3]};
-        const uint64_t strides2[3] = {64, 128, 8192};
-        const uint32_t box2[4] = {16, 1, 64, 1};
-        e = make_map_nd(&m->codes128, pk.codes, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, dims2, strides2, box2,
-                        CU_TENSOR_MAP_SWIZZLE_64B);
-    }
     if (e == cudaSuccess && pk.r > 0)
         e = make_map(&m->g, pk.G, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)pk.Kp, (uint64_t)pk.R1p, 64,
                      (uint32_t)pk.R1p, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -767,34 +654,9 @@ cudaError_t tc_prepare(const Packed &pk, TcWork &w)
     return e;
 }
 
-// Whether the forms with an epilogue take the pair kernel: its 256 x 256 tiles
-// read half as much per product, but fill the machine from 74 of them on.
-bool tc_use_pair(const Packed &pk, int64_t M, int num_sms)
-{
-    const int64_t pairs = (M + 255) / 256 * ((pk.Np + 255) / 256);
-    return M > 128 && 4 * pairs >= num_sms;
-}
-
-namespace {
-
-using TcFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, TcParams);
-template <int FORM>
-TcFn tc_fn(int BN)
-{
-    switch (BN) {
-    case 32: return tc_w4ec_kernel<32, FORM>;
-    case 64: return tc_w4ec_kernel<64, FORM>;
-    case 128: return tc_w4ec_kernel<128, FORM>;
-    default: return tc_w4ec_kernel<256, FORM>;
-    }
-}
-
-}  // namespace
-
 cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                       const TcWork &w, int *status, bool zero_wait_budget, cudaStream_t st, int num_sms,
-                      unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
-                      const float *rowc)
+                      unsigned *v_ready, unsigned v_expected)
 {
     if (M <= 0)
         return cudaSuccess;
@@ -806,21 +668,12 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
         const int bits = kStatusTimeout;
         return cudaMemcpyAsync(status, &bits, sizeof(int), cudaMemcpyHostToDevice, st);
     }
-    if (form != kPlain) {
-        const auto launch = tc_use_pair(pk, M, num_sms) ? launch_tc_pair : launch_tc_tile;
-        return launch(pk, x, y, M, v, ec, &m->bt, status, st, num_sms, v_ready, v_expected, form, epi, ldx, rowc);
-    }
     // token tile: the narrowest of 32, 64, 128, 256 that holds M (one tile row of tokens
     // up to 256), so that small batches do not run 256-wide MMAs on zero rows
     const int BN = M <= 32 ? 32 : (M <= 64 ? 64 : (M <= 128 ? 128 : 256));
     CUtensorMap tm_x, tm_v;
-    const int BK = tc_bk(form);
-    const uint64_t xd[2] = {(uint64_t)pk.K, (uint64_t)M};
-    const uint64_t xst[1] = {(uint64_t)ldx * (uint64_t)(ROW_BYTES / BK)};
-    const uint32_t xb[2] = {(uint32_t)BK, (uint32_t)BN};
-    cudaError_t e = make_map_nd(&tm_x, x, form == kQ8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                2, xd, xst, xb, CU_TENSOR_MAP_SWIZZLE_128B);
+    cudaError_t e = make_map(&tm_x, x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)pk.K, (uint64_t)M, BK,
+                             (uint32_t)BN, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess)
         return e;
     const bool use_ec = ec && pk.r > 0;
@@ -857,11 +710,12 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
     p.v_ready = use_ec ? v_ready : nullptr;
     p.v_expected = v_expected;
 
-    p.epi = epi;
-    p.rowc = rowc;
-    const TcFn fn = form == kQ8 ? tc_fn<kQ8>(BN) : (form == kEpi ? tc_fn<kEpi>(BN) : tc_fn<kPlain>(BN));
-    const int smem = tc_smem_bytes(BN, form);
-    e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
+    const void *fn = BN == 32 ? reinterpret_cast<const void *>(tc_w4ec_kernel<32>)
+                   : BN == 64 ? reinterpret_cast<const void *>(tc_w4ec_kernel<64>)
+                   : BN == 128 ? reinterpret_cast<const void *>(tc_w4ec_kernel<128>)
+                               : reinterpret_cast<const void *>(tc_w4ec_kernel<256>);
+    const int smem = tc_smem_bytes(BN);
+    e = raise_smem_limit(fn, smem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
@@ -875,8 +729,12 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const CUtensorMap &bt = use_ec ? m->bt : m->codes;
-    const CUtensorMap &codes = form == kQ8 ? m->codes128 : m->codes;
-    return cudaLaunchKernelEx(&cfg, fn, tm_x, codes, bt, tm_v, p);
+    switch (BN) {
+    case 32: return cudaLaunchKernelEx(&cfg, tc_w4ec_kernel<32>, tm_x, m->codes, bt, tm_v, p);
+    case 64: return cudaLaunchKernelEx(&cfg, tc_w4ec_kernel<64>, tm_x, m->codes, bt, tm_v, p);
+    case 128: return cudaLaunchKernelEx(&cfg, tc_w4ec_kernel<128>, tm_x, m->codes, bt, tm_v, p);
+    default: return cudaLaunchKernelEx(&cfg, tc_w4ec_kernel<256>, tm_x, m->codes, bt, tm_v, p);
+    }
 }
 
 }  // namespace spear

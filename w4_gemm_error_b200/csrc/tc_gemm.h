@@ -15,35 +15,6 @@ struct TcWork {
     int n_counters = 0;
 };
 
-// Workspace of the 8-bit form's prepass.
-struct PrepassQ8Work {
-    // two constants a token, pairs of tokens together: c0[2i], c0[2i+1], c1[2i],
-    // c1[2i+1] (rowc_at); max_M tokens rounded up to 32
-    float *rowc = nullptr;
-    float *part = nullptr;       // split-K partials
-    size_t part_floats = 0;
-    unsigned *counters = nullptr;
-    int n_counters = 0;
-};
-__host__ __device__ constexpr int64_t rowc_at(int64_t t) { return 4 * (t / 2) + (t & 1); }   // c0; c1 is 2 on
-cudaError_t prepass_q8_alloc(const Packed &pk, int64_t max_M, int num_sms, PrepassQ8Work &w);
-void prepass_q8_free(PrepassQ8Work &w);
-// rowc and (with `ec`) v of M tokens of e4m3 activations, rows ldx apart; see
-// prepass_q8.cu.  `ready` (may be null) is counted *expected times in all, once
-// per token tile when its v and rowc are written.
-cudaError_t launch_prepass_q8(const Packed &pk, const void *xq, int64_t ldx, const float *xs, int64_t M, bool ec,
-                              float *v, const PrepassQ8Work &w, cudaStream_t st, int num_sms, unsigned *ready,
-                              unsigned *expected);
-
-// The prepass of the forms kEpi and kQ8 on the tensor cores, K split over a
-// cluster (tc_prepass.cu).  xs and rowc: kQ8 alone; v: with `ec` alone; g: the
-// tensor map of G; ready, expected: as launch_prepass_q8.
-cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, const float *xs, int64_t M, bool ec,
-                               float *v, float *rowc, int form, const CUtensorMap *g, int *status, cudaStream_t st,
-                               int num_sms, unsigned *ready, unsigned *expected);
-int tc_prepass2_split(const Packed &pk, int64_t M, int num_sms);   // its CTAs per 128 tokens
-const CUtensorMap *tc_map_g(const TcWork &w);   // (of a packed layer with an EC)
-
 bool tc_available(const Packed &pk);
 cudaError_t tc_alloc(const Packed &pk, int64_t max_M, int num_sms, TcWork &w);
 void tc_free(TcWork &w);
@@ -59,25 +30,40 @@ cudaError_t launch_tc_prepass(const Packed &pk, const void *x, int64_t M, float 
 // without waiting for its predecessor, which must be a prepass that counts
 // v_expected completions into v_ready[0] and starts its dependents only once x is
 // complete; v_ready[0..1] are zero between calls.
-// form and epi: see epilogue.cuh; rows of x are ldx elements apart; rowc: the
-// prepass's per-token pair of form kQ8 (null otherwise).
 cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                       const TcWork &w, int *status, bool zero_wait_budget, cudaStream_t st, int num_sms,
-                      unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
-                      const float *rowc);
+                      unsigned *v_ready, unsigned v_expected);
 
-// The forms kEpi and kQ8 (launch_tc takes them): pairs of CTAs on 256 x 256
-// tiles (tc_pair.cu), or one CTA on 128 x up to 128 with K split over a cluster
-// (tc_tile.cu).  bt: the tensor map of B^T/e; rowc holds whole chunks of 32
-// tokens.
+// ---- the forms kEpi and kQ8 of epilogue.cuh
+
+// Two constants a token of form kQ8, 2^9 xs[t] and 2^-9 sum_k xq[t,k], pairs of
+// tokens together (c0[2i], c0[2i+1], c1[2i], c1[2i+1]); whole chunks of 32
+// tokens are allocated.  Index of c0; c1 is 2 on.
+__host__ __device__ constexpr int64_t rowc_at(int64_t t) { return 4 * (t / 2) + (t & 1); }
+inline size_t rowc_floats(int64_t max_M) { return (size_t)((max_M + 31) / 32 * 32) * 2; }
+
+struct Epilogue;
+const CUtensorMap *tc_map_g(const TcWork &w);    // tensor maps of G and of B^T/e
+const CUtensorMap *tc_map_bt(const TcWork &w);   // (of a packed layer with an EC)
+
+// Prepass on the tensor cores, K split over a cluster (tc_prepass.cu): v with
+// `ec`, rowc in form kQ8 (xs: its scales).  Rows of x are ldx elements apart.
+// `ready` (may be null) is counted *expected times in all, once per CTA when
+// what it writes is there.
+int tc_prepass2_split(const Packed &pk, int64_t M, int num_sms);   // CTAs per 128 tokens
+cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, const float *xs, int64_t M, bool ec,
+                               float *v, float *rowc, int form, const CUtensorMap *g, int *status, cudaStream_t st,
+                               int num_sms, unsigned *ready, unsigned *expected);
+
+// The product and epilogue: pairs of CTAs on 256 x 256 tiles (tc_pair.cu, which
+// reads rowc), or one CTA on 128 x up to 128 with K split over a cluster
+// (tc_tile.cu, which sums the codes itself).  v_ready, v_expected: as launch_tc.
 bool tc_use_pair(const Packed &pk, int64_t M, int num_sms);
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
-                           const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,
-                           unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
-                           const float *rowc);
+                           const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms, unsigned *v_ready,
+                           unsigned v_expected, int form, const Epilogue &epi, int64_t ldx, const float *rowc);
 cudaError_t launch_tc_tile(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
-                           const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,
-                           unsigned *v_ready, unsigned v_expected, int form, const Epilogue &epi, int64_t ldx,
-                           const float *rowc);
+                           const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms, unsigned *v_ready,
+                           unsigned v_expected, int form, const Epilogue &epi, int64_t ldx);
 
 }  // namespace spear

@@ -84,7 +84,7 @@ struct PairParams {
     unsigned *v_ready;       // as TcParams::v_ready (tc_gemm.cu)
     unsigned v_expected;
     Epilogue epi;
-    const float *rowc;       // form kQ8: as TcParams::rowc, padded to whole chunks
+    const float *rowc;       // form kQ8: the constants of rowc_at, whole chunks
 };
 
 // One slot's outputs of this thread: channel n (row `row` of the CTA), the 32
@@ -551,6 +551,15 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PairParams);
 
 }  // namespace
+
+// Whether the forms with an epilogue take these kernels' 256 x 256 tiles: they
+// read half as much per product as the 128 x 128 ones of tc_tile.cu, but leave
+// SMs idle below half a machine of pairs.
+bool tc_use_pair(const Packed &pk, int64_t M, int num_sms)
+{
+    const int64_t pairs = (M + BN - 1) / BN * ((pk.Np + 2 * BM - 1) / (2 * BM));
+    return M > 128 && 4 * pairs >= num_sms;
+}
 
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                            const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms,

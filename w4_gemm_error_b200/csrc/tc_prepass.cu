@@ -1,6 +1,6 @@
 // Gate and EC down-projection of many tokens on the tensor cores, K split over
 // a cluster: what the forms kEpi and kQ8 of the forward pass need of each token
-// before their epilogue (see prepass.cu and prepass_q8.cu for the formulas).
+// before their epilogue (see prepass.cu for g and v).
 //
 //   D[t, j] = x[t,:] . G[j,:],  G = [w_g; A^T] (R1p rows)
 //   kEpi: v = g D[t,1+j],         g = 1 / (1 + exp(-(D[t,0] + b_g)))

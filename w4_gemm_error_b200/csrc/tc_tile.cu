@@ -206,6 +206,7 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             if (!warp_wait(ready0 + 8 * slot, phase, &abort_flag, p.status))
                 break;
             const uint8_t *xt = bp + slot * STAGE_BYTES + A_BYTES;
+            uint32_t seen = 0u;
 #pragma unroll
             for (int g = 0; g < BN / 32; ++g)
 #pragma unroll
@@ -215,12 +216,13 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                     const int row = 8 * (w + 4 * g) + gid;
                     const uint4 v = *reinterpret_cast<const uint4 *>(xt + row * kTcRowBytes + (((4 * h + cl) ^ gid) << 4));
                     const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+                    seen ^= v.x ^ v.w;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         mma_f16_16816(xsum[g], kOnes, kOnes, kOnes, kOnes, e4m3x2_to_f16x2((uint16_t)c[j]),
                                       e4m3x2_to_f16x2((uint16_t)(c[j] >> 16)));
                 }
-            __syncwarp();
+            loads_complete(seen);
             if (lane == 0)
                 mbar_arrive(empty0 + 8 * slot);
             if (++slot == STAGES) {
@@ -228,12 +230,8 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 phase ^= 1;
             }
         }
-        for (int i = nm; i < nst; ++i) {   // (EC stages)
-            if (lane == 0)
-                mbar_arrive(empty0 + 8 * slot);
-            if (++slot == STAGES)
-                slot = 0;
-        }
+        // (the EC stages, at most four of the ring's six or more, are its last: nothing
+        // waits for their slots to be free again)
     } else if (warp >= DEQ_WARP) {
         const int grp = (warp - DEQ_WARP) / GROUP_WARPS, w = warp & 3;
         TcDequant<FORM> d(w, lane);
@@ -384,7 +382,7 @@ TileFn tile_fn(int BN)
 
 cudaError_t launch_tc_tile(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                            const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms, unsigned *v_ready,
-                           unsigned v_expected, int form, const Epilogue &epi, int64_t ldx, const float *)
+                           unsigned v_expected, int form, const Epilogue &epi, int64_t ldx)
 {
     const int BN = M <= 32 ? 32 : (M <= 64 ? 64 : 128);
     const int BK = tc_stage_k(form);
