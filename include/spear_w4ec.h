@@ -385,6 +385,35 @@ int spear_w4ec_stack_forward(spear_w4ec_stack *s, const void *x, void *y, int64_
 int spear_w4ec_stack_forward_host(spear_w4ec_stack *s, const void *x_host, void *y_host, int64_t M,
                                   uint32_t flags, void *stream);
 
+/* What one op of a stack does around its layer (SPEAR_ACT_* and the formulas
+ * as in spear_w4ec_epilogue and spear_w4ec_rmsnorm):
+ *   a    = the op's input buffer, or its root-mean-square norm
+ *   (q8) a in 8 bits with one scale a token, the layer run on those
+ *   out  = act(Y(a) + bias) * mul + residual
+ * so that a decoder's blocks run as one stack: the norm in front of q, k, v and
+ * of gate and up; the activated gate projection as the multiplier of up; the
+ * residual stream added by o and down. */
+typedef struct spear_w4ec_stack_ext {
+    const void *norm_weight; /* dev bf16 [K of the op], or NULL: no norm */
+    float norm_eps;
+    int32_t q8;              /* 1: 8-bit activations */
+    const void *bias;        /* dev bf16 [N], or NULL */
+    int32_t act;             /* SPEAR_ACT_* */
+    int32_t mul;             /* buffer [M][N] (0: the stack's input; never 1), or -1 */
+    int32_t residual;        /* buffer [M][N], likewise, or -1; may be the buffer the op writes */
+} spear_w4ec_stack_ext;
+
+/* Set what op `op` (0 .. n_ops - 1) does around its layer from now on; NULL:
+ * nothing, as created.  norm_weight and bias are not copied: they must stay
+ * valid while the stack is used.  Buffers are numbered as in
+ * spear_w4ec_stack_create and must have been written by an earlier op with the
+ * width N of this one (SPEAR_ERR_INVALID otherwise).  Ops in a row that read one
+ * buffer with one norm share its result.  Allocates scratch for the stack's
+ * normed or 8-bit activations at the first op that needs it.  An op that was set
+ * runs as spear_w4ec_forward_ep / _forward_q8 (same flags); a stack with one
+ * does not run as SPEAR_STACK_PERSISTENT (SPEAR_ERR_UNSUPPORTED). */
+int spear_w4ec_stack_set_op(spear_w4ec_stack *s, int32_t op, const spear_w4ec_stack_ext *ext);
+
 /* Device address of intermediate buffer `index` (>= 2) in *ptr: after a
  * forward on M tokens it holds the [M][width] output of the last op that
  * wrote it (for inspection and tests). */

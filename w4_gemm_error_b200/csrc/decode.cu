@@ -425,7 +425,7 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 }
             }
             // every lane's shared-memory reads of this stage are done: release it
-            if constexpr (FORM != kPlain)
+            if constexpr (FORM == kQ8)
                 loads_complete(seen);
             __syncwarp();
             if (lane == 0)
@@ -486,7 +486,7 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                                        ha[2 * q + 1], xa[2 * q], xa[2 * q + 1]);
                 }
             }
-            if constexpr (FORM != kPlain)
+            if constexpr (FORM == kQ8)
                 loads_complete(seen);
             __syncwarp();
             if (lane == 0)

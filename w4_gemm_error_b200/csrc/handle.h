@@ -99,4 +99,10 @@ bool path_supported(const spear_w4ec *h, uint32_t path);
 // made the handle's device current.
 int forward_checked(const spear_w4ec *h, const void *x, void *y, int64_t M, uint32_t flags, cudaStream_t st);
 
+// The same with an epilogue, on bf16 activations (xs null) or e4m3 ones with
+// their scales.
+struct Epilogue;
+int forward_ep_checked(const spear_w4ec *h, const void *x, const float *xs, void *y, int64_t M, uint32_t flags,
+                       cudaStream_t st, const Epilogue &epi);
+
 }  // namespace spear

@@ -418,6 +418,20 @@ int forward_checked(const spear_w4ec *h, const void *x, void *y, int64_t M, uint
     return run_forward(h, x, y, M, flags, st);
 }
 
+int forward_ep_checked(const spear_w4ec *h, const void *x, const float *xs, void *y, int64_t M, uint32_t flags,
+                       cudaStream_t st, const Epilogue &epi)
+{
+    if (xs)
+        return run_forward_q8(h, x, xs, y, M, flags, st, epi);
+    // nothing after the layer: the plain forward, its EC in the product's kernel
+    if (!epi.bias && !epi.mul && !epi.residual && epi.act == kActNone) {
+        if (flags & SPEAR_FORCE_SPLIT)
+            return SPEAR_ERR_UNSUPPORTED;
+        return run_forward(h, x, y, M, flags | SPEAR_FORCE_FUSED, st);
+    }
+    return run_forward(h, x, y, M, flags, st, kEpi, epi);
+}
+
 }  // namespace spear
 
 extern "C" {
@@ -573,13 +587,7 @@ int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M
     DeviceGuard guard(h->device);
     if (!guard.ok())
         return SPEAR_ERR_CUDA;
-    // nothing after the layer: the plain forward, its EC in the product's kernel
-    if (!epi.bias && !epi.mul && !epi.residual && epi.act == kActNone) {
-        if (flags & SPEAR_FORCE_SPLIT)
-            return SPEAR_ERR_UNSUPPORTED;
-        return run_forward(h, x, y, M, flags | SPEAR_FORCE_FUSED, static_cast<cudaStream_t>(stream));
-    }
-    return run_forward(h, x, y, M, flags, static_cast<cudaStream_t>(stream), kEpi, epi);
+    return forward_ep_checked(h, x, nullptr, y, M, flags, static_cast<cudaStream_t>(stream), epi);
 }
 
 int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y, int64_t M,
@@ -603,7 +611,7 @@ int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, 
     DeviceGuard guard(h->device);
     if (!guard.ok())
         return SPEAR_ERR_CUDA;
-    return run_forward_q8(h, xq, xs, y, M, flags, static_cast<cudaStream_t>(stream), epi);
+    return forward_ep_checked(h, xq, xs, y, M, flags, static_cast<cudaStream_t>(stream), epi);
 }
 
 int spear_w4ec_forward_host(spear_w4ec *h, const void *x_host, void *y_host, int64_t M, uint32_t flags,

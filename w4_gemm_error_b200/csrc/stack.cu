@@ -12,7 +12,9 @@
 #include <new>
 #include <vector>
 
+#include "epilogue.cuh"
 #include "handle.h"
+#include "norm.h"
 #include "tensor_map.h"
 #include "spear_w4ec.h"
 
@@ -35,6 +37,16 @@ struct spear_w4ec_stack {
     CUtensorMap *p_maps = nullptr;         // device [n_ops][2]
     unsigned *p_ws = nullptr;              // device: [2 n_ops] counters, then the u accumulators
     size_t p_ws_bytes = 0;
+    // what spear_w4ec_stack_set_op added to the ops, and its scratch (max_M rows
+    // of the widest input that is normed or quantised)
+    struct Extra {
+        bool on = false;
+        spear_w4ec_stack_ext ext{};
+    };
+    std::vector<Extra> extras;   // empty: none
+    void *norm_buf = nullptr;    // bf16
+    void *q_buf = nullptr;       // e4m3
+    float *q_scale = nullptr;
 };
 
 namespace {
@@ -50,6 +62,9 @@ void free_stack(spear_w4ec_stack *s)
     cudaFree(s->p_ops);
     cudaFree(s->p_maps);
     cudaFree(s->p_ws);
+    cudaFree(s->norm_buf);
+    cudaFree(s->q_buf);
+    cudaFree(s->q_scale);
 }
 
 // The persistent kernel's plan: per op its operands, buffers, the op it must
@@ -142,6 +157,9 @@ int run_persistent(spear_w4ec_stack *s, const void *x, void *y, int64_t M, uint3
 {
     if (!s->persist || M > kStackMaxTokens || (flags & kPathFlags))
         return SPEAR_ERR_UNSUPPORTED;
+    for (const auto &x : s->extras)
+        if (x.on)
+            return SPEAR_ERR_UNSUPPORTED;   // that kernel runs bare layers
     if (s->fault_launch)
         return SPEAR_ERR_CUDA;
     unsigned *done = s->p_ws;
@@ -158,13 +176,47 @@ int run_ops(spear_w4ec_stack *s, const void *x, void *y, int64_t M, uint32_t fla
 {
     if (flags & SPEAR_STACK_PERSISTENT)
         return run_persistent(s, x, y, M, flags & ~(uint32_t)SPEAR_STACK_PERSISTENT, st);
-    for (const spear_w4ec_stack_op &op : s->ops) {
+    // the op whose normed (bf16) and whose 8-bit input the scratch holds (-1: none)
+    int held[2] = {-1, -1};
+    for (size_t i = 0; i < s->ops.size(); ++i) {
+        const spear_w4ec_stack_op &op = s->ops[i];
         const void *in = op.in == 0 ? x : s->bufs[op.in];
         void *out = op.out == 1 ? y : s->bufs[op.out];
         const uint32_t f = flags | (op.ec ? 0u : (uint32_t)SPEAR_EC_OFF);
-        const int rc = forward_checked(op.layer, in, out, M, f, st);
+        int rc;
+        if (s->extras.empty() || !s->extras[i].on) {
+            rc = forward_checked(op.layer, in, out, M, f, st);
+        } else {
+            const spear_w4ec_stack_ext &e = s->extras[i].ext;
+            const bool prepare = e.norm_weight || e.q8;
+            int &h = held[e.q8 ? 1 : 0];
+            // ops that read one buffer with one norm (q, k and v; gate and up) share its result
+            const bool same = h >= 0 && s->ops[h].in == op.in && s->extras[h].ext.norm_weight == e.norm_weight &&
+                              s->extras[h].ext.norm_eps == e.norm_eps;
+            if (prepare && !same) {
+                const cudaError_t c = launch_norm(in, nullptr, e.norm_weight, e.norm_eps, M, op.layer->pk.K, nullptr,
+                                                  e.q8 ? nullptr : s->norm_buf, e.q8 ? s->q_buf : nullptr,
+                                                  e.q8 ? s->q_scale : nullptr, st);
+                if (c != cudaSuccess)
+                    return status_of(c);
+                h = (int)i;
+            }
+            auto buffer = [&](int32_t b) {
+                return static_cast<const uint16_t *>(b < 0 ? nullptr : (b == 0 ? x : s->bufs[b]));
+            };
+            Epilogue epi;
+            epi.bias = static_cast<const uint16_t *>(e.bias);
+            epi.mul = buffer(e.mul);
+            epi.residual = buffer(e.residual);
+            epi.act = e.act;
+            rc = forward_ep_checked(op.layer, e.q8 ? s->q_buf : (prepare ? s->norm_buf : in), e.q8 ? s->q_scale : nullptr,
+                                    out, M, f, st, epi);
+        }
         if (rc != SPEAR_OK)
             return rc;
+        for (int &h : held)
+            if (h >= 0 && s->ops[h].in == op.out)
+                h = -1;   // its source was overwritten
     }
     return SPEAR_OK;
 }
@@ -291,6 +343,63 @@ int spear_w4ec_stack_forward_host(spear_w4ec_stack *s, const void *x_host, void 
     if (e == cudaSuccess)
         e = cudaStreamSynchronize(st);
     return status_of(e);
+}
+
+int spear_w4ec_stack_set_op(spear_w4ec_stack *s, int32_t op, const spear_w4ec_stack_ext *ext)
+{
+    if (!s || op < 0 || op >= (int32_t)s->ops.size())
+        return SPEAR_ERR_INVALID;
+    const int32_t n_bufs = (int32_t)s->bufs.size();
+    const Packed &pk = s->ops[op].layer->pk;
+    if (ext) {
+        if (ext->act < SPEAR_ACT_NONE || ext->act > SPEAR_ACT_GELU_TANH || (ext->q8 != 0 && ext->q8 != 1) ||
+            !aligned16(ext->norm_weight) || !aligned16(ext->bias))
+            return SPEAR_ERR_INVALID;
+        if (ext->norm_weight && !(ext->norm_eps >= 0.0f && ext->norm_eps < 1e30f))
+            return SPEAR_ERR_INVALID;
+        // the width that each buffer has when the op runs
+        std::vector<int64_t> width(n_bufs, 0);
+        width[0] = s->in_width;
+        for (int32_t i = 0; i < op; ++i)
+            width[s->ops[i].out] = s->ops[i].layer->pk.N;
+        for (int32_t b : {ext->mul, ext->residual})
+            if (b != -1 && (b < 0 || b == 1 || b >= n_bufs || width[b] != pk.N))
+                return SPEAR_ERR_INVALID;
+    }
+    DeviceGuard guard(s->device);
+    if (!guard.ok())
+        return SPEAR_ERR_CUDA;
+    // scratch for the widest input of any op (an op may get its norm later)
+    cudaError_t e = cudaSuccess;
+    int64_t widest = 0;
+    for (const spear_w4ec_stack_op &o : s->ops)
+        widest = std::max(widest, o.layer->pk.K);
+    if (ext && ext->q8 && !s->q_buf) {
+        void *q = nullptr;
+        e = cudaMalloc(&q, (size_t)s->max_M * (size_t)widest);
+        if (e == cudaSuccess)
+            e = cudaMalloc(&s->q_scale, (size_t)s->max_M * sizeof(float));
+        if (e != cudaSuccess) {
+            cudaFree(q);
+            s->q_scale = nullptr;
+            cudaGetLastError();
+            return status_of(e);
+        }
+        s->q_buf = q;
+    }
+    if (ext && ext->norm_weight && !ext->q8 && !s->norm_buf) {
+        e = cudaMalloc(&s->norm_buf, (size_t)s->max_M * (size_t)widest * 2);
+        if (e != cudaSuccess) {
+            s->norm_buf = nullptr;
+            cudaGetLastError();
+            return status_of(e);
+        }
+    }
+    if (s->extras.empty())
+        s->extras.resize(s->ops.size());
+    s->extras[op].on = ext != nullptr;
+    s->extras[op].ext = ext ? *ext : spear_w4ec_stack_ext{};
+    return SPEAR_OK;
 }
 
 int spear_w4ec_stack_buffer(const spear_w4ec_stack *s, int32_t index, void **ptr)

@@ -48,7 +48,7 @@ EXPORTED = ("spear_w4ec_create", "spear_w4ec_pack", "spear_w4ec_pack_asym", "spe
             "spear_w4ec_destroy", "spear_w4ec_get_packed", "spear_w4ec_get_gate", "spear_w4ec_sync_status",
             "spear_w4ec_tune", "spear_w4ec_dispatch", "spear_w4ec_gate_noalloc", "spear_w4ec_set_next",
             "spear_w4ec_stack_create", "spear_w4ec_stack_forward", "spear_w4ec_stack_forward_host",
-            "spear_w4ec_stack_buffer", "spear_w4ec_stack_destroy", "spear_w4ec_cost", "spear_w4ec_table_save",
+            "spear_w4ec_stack_buffer", "spear_w4ec_stack_set_op", "spear_w4ec_stack_destroy", "spear_w4ec_cost", "spear_w4ec_table_save",
             "spear_w4ec_table_load", "spear_w4ec_tp_create", "spear_w4ec_tp_buffer", "spear_w4ec_tp_ipc_handle",
             "spear_w4ec_tp_connect_ipc", "spear_w4ec_tp_connect", "spear_w4ec_tp_partial", "spear_w4ec_tp_reduce",
             "spear_w4ec_tp_forward", "spear_w4ec_tp_destroy", "spear_w4ec_strerror")
@@ -75,6 +75,13 @@ class StackOp(ctypes.Structure):
     and whether its EC is placed (1) or not (0)."""
     _fields_ = [("layer", ctypes.c_void_p), ("in_", ctypes.c_int32), ("out", ctypes.c_int32),
                 ("ec", ctypes.c_int32)]
+
+
+class StackExt(ctypes.Structure):
+    """spear_w4ec_stack_ext: what an op of a stack does around its layer."""
+    _fields_ = [("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float), ("q8", ctypes.c_int32),
+                ("bias", ctypes.c_void_p), ("act", ctypes.c_int32), ("mul", ctypes.c_int32),
+                ("residual", ctypes.c_int32)]
 
 
 def _load():
@@ -105,6 +112,7 @@ def _load():
         "spear_w4ec_stack_forward": [P, P, P, i64, u32, P],
         "spear_w4ec_stack_forward_host": [P, P, P, i64, u32, P],
         "spear_w4ec_stack_buffer": [P, i32, ctypes.POINTER(P)],
+        "spear_w4ec_stack_set_op": [P, i32, ctypes.POINTER(StackExt)],
         "spear_w4ec_stack_destroy": [P],
         "spear_w4ec_cost": [P, i64, u32, ctypes.POINTER(f32)],
         "spear_w4ec_table_save": [P, ctypes.c_char_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)],
@@ -294,6 +302,11 @@ def spear_w4ec_stack_buffer(s: int, index: int) -> int:
     p = ctypes.c_void_p()
     _check(_lib.spear_w4ec_stack_buffer(s, index, ctypes.byref(p)), "spear_w4ec_stack_buffer")
     return p.value
+
+
+def spear_w4ec_stack_set_op(s: int, op: int, ext=None):
+    """ext: a StackExt, or None (the op runs its bare layer)."""
+    _check(_lib.spear_w4ec_stack_set_op(s, op, None if ext is None else ctypes.byref(ext)), "spear_w4ec_stack_set_op")
 
 
 def spear_w4ec_stack_destroy(s: int):
@@ -616,6 +629,28 @@ class W4ECStack:
         self.widths = {}
         for lin, _, o, _ in ops:
             self.widths[o] = lin.N
+        self._set = {}   # tensors that the stack's ops point to
+
+    def set_op(self, op: int, *, norm: torch.Tensor | None = None, eps: float = 1e-6, q8: bool = False,
+               bias: torch.Tensor | None = None, act: str = "none", mul: int | None = None,
+               residual: int | None = None):
+        """What op number ``op`` does around its layer from now on: the norm of its
+        input (weight bf16 [K]), 8-bit activations, bias (bf16 [N]), activation, and
+        the numbers of the buffers that multiply and are added to its output.
+        Called with the number alone: nothing again."""
+        lin = self.layers[op]
+        try:
+            code = ACTIVATIONS[act]
+        except (KeyError, TypeError):
+            raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}") from None
+        dev = self.device.index
+        w = None if norm is None else _dev(norm, torch.bfloat16, (lin.K,), "norm", dev)
+        b = None if bias is None else _dev(bias, torch.bfloat16, (lin.N,), "bias", dev)
+        plain = not (w or q8 or b or code) and mul is None and residual is None
+        ext = None if plain else StackExt(w, eps, int(q8), b, code, -1 if mul is None else mul,
+                                          -1 if residual is None else residual)
+        spear_w4ec_stack_set_op(self.h, op, ext)
+        self._set[op] = (norm, bias)
 
     def forward(self, x: torch.Tensor, flags: int = 0, out: torch.Tensor | None = None, stream=None):
         M = x.shape[0]
