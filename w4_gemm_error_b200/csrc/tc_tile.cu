@@ -12,10 +12,11 @@
 // rank: v and B^T/e), warp 1 issues the MMAs, warp 2 asks for the CTA's codes
 // from HBM to L2 (all of them at once, before anything else: they depend on no
 // earlier kernel), warps 8-23 dequantise (four groups taking every fourth stage,
-// tc_dequant.cuh).  Warps 4-7 read the accumulator at the end; in form kQ8 they
-// sum the codes of each token until then (mma.sync of the staged activations,
-// made f16, with a tile of ones: exact products), so that a layer without the
-// Error Compensator needs no prepass.
+// tc_dequant.cuh), warps 4-7 read the accumulator at the end.  In form kQ8 every
+// stage also multiplies its tokens with a constant tile of ones (64 rows, into
+// TMEM columns of their own): the code sums that the zero points need, so that a
+// layer without the Error Compensator needs no prepass.  (Summed by four warps
+// with mma.sync instead, the sums lagged six stages behind the product.)
 // Then all of them take the outputs of the CTA's 1/S of the tokens, two channels a
 // thread: the S partials, the epilogue, 4-byte stores of whole lines.
 // Every wait is bounded (about a second); one that runs out sets the handle's
@@ -38,7 +39,11 @@ constexpr int THREADS = 32 * (DEQ_WARP + GROUPS * GROUP_WARPS);
 constexpr int kMaxSplit = 8;
 __host__ __device__ constexpr int tile_stage_bytes(int BN) { return A_BYTES + BN * kTcRowBytes; }
 __host__ __device__ constexpr int tile_stages(int BN) { return BN == 128 ? 6 : 8; }
-__host__ __device__ constexpr int tile_smem_bytes(int BN) { return tile_stages(BN) * tile_stage_bytes(BN) + 1024; }
+constexpr int ONES_BYTES = 64 * kTcRowBytes;   // form kQ8: the tile of ones
+__host__ __device__ constexpr int tile_smem_bytes(int BN)
+{
+    return tile_stages(BN) * tile_stage_bytes(BN) + ONES_BYTES + 1024;
+}
 
 struct TileParams {
     int64_t M, N, Np;
@@ -64,6 +69,8 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     constexpr int STAGES = tile_stages(BN);
     constexpr int B_BYTES = BN * kTcRowBytes;
     constexpr int STAGE_BYTES = tile_stage_bytes(BN);
+    constexpr int TMEM_COLS = FORM == kQ8 ? 2 * BN : BN;   // the accumulator, the code sums
+    constexpr uint32_t ONES = STAGES * STAGE_BYTES;        // byte offset of the tile of ones
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * STAGES + 2];   // ready and empty of each stage; done; drain
     __shared__ uint32_t tmem_base_slot;
@@ -84,7 +91,7 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         abort_flag = 0;
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(ready0 + 8 * s, GROUP_WARPS + 1);
-            mbar_init(empty0 + 8 * s, FORM == kQ8 ? 1 + 4 : 1);   // the MMAs, the warps that sum
+            mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(done, 1);
         mbar_init(drain, 1);
@@ -100,16 +107,20 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(&tmem_base_slot)),
-                     "r"(BN)
+                     "r"(TMEM_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if constexpr (FORM == kQ8) {
+        for (int i = tid; i < ONES_BYTES / 16; i += THREADS)   // (1.0 in e4m3; any order will do)
+            reinterpret_cast<uint4 *>(bp + ONES)[i] = make_uint4(0x38383838u, 0x38383838u, 0x38383838u, 0x38383838u);
+        fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_slot;
     pdl_launch_dependents();   // (after the tensor memory is held: see the prepass)
-    float xsum[BN / 32][4] = {};   // form kQ8, warps 4-7
 
     if (warp == 0) {
         const bool elected = elect_one();
@@ -154,7 +165,9 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         const uint32_t shape = ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24) | (1u << 4);
         const uint32_t idesc = shape | (FORM == kQ8 ? 0u : (1u << 7) | (1u << 10));
         const uint32_t idesc_tf32 = shape | (2u << 7) | (2u << 10);
+        const uint32_t idesc_ones = ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(64 >> 4) << 24) | (1u << 4);
         const uint64_t a0 = smem_desc_sw128(base), b0 = smem_desc_sw128(base + A_BYTES);
+        const uint64_t ones = smem_desc_sw128(base + ONES);
         uint32_t slot = 0, phase = 0;
         bool ok = true;
         for (int i = 0; i < nst; ++i) {
@@ -174,6 +187,8 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                             mma_e4m3(tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
                         else
                             mma_bf16(tmem, a_desc + 2 * k, b_desc + 2 * k, idesc, accumulate);
+                        if constexpr (FORM == kQ8)
+                            mma_e4m3(tmem + BN, ones, b_desc + 2 * k, idesc_ones, accumulate);
                     }
                     mma_commit(empty0 + 8 * slot);
                 }
@@ -197,41 +212,6 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         }
         __syncwarp();
         mbar_wait_final(drain, 0);
-    } else if (FORM == kQ8 && warp >= 4 && warp < DEQ_WARP) {
-        // sums of the codes: this warp the groups of eight tokens w, w + 4, ...
-        const int w = warp & 3, gid = lane >> 2, cl = lane & 3;
-        constexpr uint32_t kOnes = 0x3C003C00u;
-        uint32_t slot = 0, phase = 0;
-        for (int i = 0; i < nm; ++i) {
-            if (!warp_wait(ready0 + 8 * slot, phase, &abort_flag, p.status))
-                break;
-            const uint8_t *xt = bp + slot * STAGE_BYTES + A_BYTES;
-            uint32_t seen = 0u;
-#pragma unroll
-            for (int g = 0; g < BN / 32; ++g)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // 16 codes of token 8 (w + 4 g) + gid (any order of k will do; the rotation
-                    // spreads the tokens over the banks)
-                    const int row = 8 * (w + 4 * g) + gid;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(xt + row * kTcRowBytes + (((4 * h + cl) ^ gid) << 4));
-                    const uint32_t c[4] = {v.x, v.y, v.z, v.w};
-                    seen ^= v.x ^ v.w;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_f16_16816(xsum[g], kOnes, kOnes, kOnes, kOnes, e4m3x2_to_f16x2((uint16_t)c[j]),
-                                      e4m3x2_to_f16x2((uint16_t)(c[j] >> 16)));
-                }
-            loads_complete(seen);
-            if (lane == 0)
-                mbar_arrive(empty0 + 8 * slot);
-            if (++slot == STAGES) {
-                slot = 0;
-                phase ^= 1;
-            }
-        }
-        // (the EC stages, at most four of the ring's six or more, are its last: nothing
-        // waits for their slots to be free again)
     } else if (warp >= DEQ_WARP) {
         const int grp = (warp - DEQ_WARP) / GROUP_WARPS, w = warp & 3;
         TcDequant<FORM> d(w, lane);
@@ -279,11 +259,14 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             for (int j = 0; j < 16; ++j)
                 part[(c + j) * BM + 32 * q + lane] = ok ? __uint_as_float(a[j]) : 0.f;
         }
-        if (FORM == kQ8 && lane < 4)   // (every row of the ones' product is the sum)
+        if (FORM == kQ8 && q == 0)   // (every row of the ones' product is the sums; the first is lane 0's)
+            for (int c = 0; c < BN && t0 + c < p.M; c += 16) {
+                uint32_t a[16];
+                tmem_ld_32x32b_x16(tmem + BN + c, a);
+                if (lane == 0)
 #pragma unroll
-            for (int g = 0; g < BN / 32; ++g) {
-                part[BN * BM + 8 * (q + 4 * g) + 2 * lane] = xsum[g][0];
-                part[BN * BM + 8 * (q + 4 * g) + 2 * lane + 1] = xsum[g][1];
+                    for (int j = 0; j < 16; ++j)
+                        part[BN * BM + c + j] = __uint_as_float(a[j]);
             }
         tc_fence_before();
     }
@@ -296,7 +279,8 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(BN) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                     : "memory");
     }
 
     // ---- outputs: this CTA's tokens, two channels a thread
