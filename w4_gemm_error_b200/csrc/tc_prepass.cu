@@ -28,8 +28,12 @@ namespace {
 
 constexpr int kTok = 128;
 constexpr int kMaxStages = 8;
-constexpr int kConvWarps = 8;      // warps 2-9: conversion (kQ8), then the accumulator (the first four)
-constexpr int kThreads = 64 + 32 * kConvWarps;
+// Warps 2-17: two groups of eight, converting every second block (kQ8), then all
+// reading the accumulator.  The ring has an even number of stages, so that a
+// stage always belongs to one group: a group that skipped a phase of a barrier
+// could take the phase before it, of the same parity, for its own.
+constexpr int kGroups = 2;
+constexpr int kThreads = 64 + 256 * kGroups;
 constexpr int kMaxCluster = 8;
 constexpr int kOnesRows = 16;      // kQ8: rows of ones after those of G, whose product is X_t
 
@@ -99,7 +103,7 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         abort_flag = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full0 + 8 * s, 1);
-            mbar_init(staged0 + 8 * s, kConvWarps);
+            mbar_init(staged0 + 8 * s, 8);
             mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(done, 1);
@@ -135,7 +139,7 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // and this CTA holds its tensor memory
     pdl_launch_dependents();
 
-    const int q = warp & 3, row = 32 * q + lane;   // warps 2-5: TMEM lane = token of the tile
+    const int q = warp & 3, row = 32 * q + lane;   // warps 2 and up: TMEM lane = token of the tile
     if (warp == 0) {
         if (lane == 0) {
             int issued = 0;
@@ -191,17 +195,17 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         mbar_wait_final(drain, 0);
     } else if (FORM == kQ8) {
         // e4m3 -> bf16: half of one token's 64 k a thread
-        const int half = (warp - 2) >> 2;
-        uint32_t slot = 0, phase = 0;
-        for (int i = 0; i < nkb; ++i) {
+        const int grp = (warp - 2) >> 3, half = ((warp - 2) >> 2) & 1;
+        int slot = grp;   // (the ring has at least two stages)
+        uint32_t phase = 0;
+        for (int i = grp; i < nkb; i += kGroups) {
             if (!warp_wait(full0 + 8 * slot, phase, &abort_flag, p.status))
                 break;
             uint8_t *const sb = bp + slot * sbytes;
             const uint8_t *src = sb + kXin + row * 64;
             uint8_t *dst = sb + row * 128;
 #pragma unroll
-            for (int c2 = 0; c2 < 2; ++c2) {
-                const int c = 2 * half + c2;
+            for (int c = 2 * half; c < 2 * half + 2; ++c) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(src + ((c ^ ((row >> 1) & 3)) << 4));
                 const uint32_t words[4] = {w.x, w.y, w.z, w.w};
                 uint32_t o[8];
@@ -217,8 +221,9 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(staged0 + 8 * slot);
-            if ((int)++slot == kStages) {
-                slot = 0;
+            slot += kGroups;
+            if (slot >= kStages) {   // (an even ring: back to this group's first)
+                slot -= kStages;
                 phase ^= 1;
             }
         }
@@ -226,14 +231,14 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 
     // ---- this CTA's partial: [token][R1p columns of D, X], rows of whole 16 bytes
     const int ld = p.R1p + 4;
-    const bool reader = warp >= 2 && warp < 6;
+    const bool reader = warp >= 2;   // quarter q: the tokens 32 q ..; four warps a quarter, columns 16 at a time
     float *const part = reinterpret_cast<float *>(bp);
     const bool got = !reader || mbar_wait(done, 0, &abort_flag, p.status);
     __syncthreads();   // every copy and MMA of this CTA is over: the stages are free
     if (reader) {
         tc_fence_after();
         __syncwarp();
-        for (int c = 0; c < ncol; c += 16) {
+        for (int c = 16 * ((warp - 2) >> 2); c < ncol; c += 64) {
             uint32_t a[16];
             tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * q) << 16) + c, a);
 #pragma unroll
@@ -350,7 +355,7 @@ cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, con
     if (expected)
         *expected = (unsigned)(tiles * S);
     const size_t stage = q8 ? stage_bytes<kQ8>(p.R1p) : stage_bytes<kEpi>(p.R1p);
-    p.stages = (int)std::min<size_t>(kMaxStages, 220 * 1024 / stage);
+    p.stages = (int)std::min<size_t>(kMaxStages, 220 * 1024 / stage) & ~1;   // even
     const size_t ring = p.stages * stage;
     const size_t part = (size_t)(kTok + (kTok + S - 1) / S) * (p.R1p + 4) * sizeof(float);   // partials, then sums
     const size_t smem = std::max(ring, part) + 1024;
