@@ -191,7 +191,8 @@ int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, 
  *   y[t,k] = bf16(v[t,k])
  *   s[t]   = a_t / 448,  q[t,k] = e4m3(v[t,k] * (448 / a_t)),
  *            a_t = max(max_k |v[t,k]|, 2^-100)
- * in fp32, each output rounded once (to nearest even).  (q, s) is what
+ * in fp32, each output rounded once (to nearest even; a row of zeros with
+ * eps = 0 is 0 / 0).  (q, s) is what
  * spear_w4ec_forward_q8 takes.  A row with an infinity or NaN has a scale that
  * is not finite, or NaN outputs.
  *   x, residual, sum, y   dev bf16 [M][K]   weight  dev bf16 [K]

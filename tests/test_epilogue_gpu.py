@@ -45,7 +45,10 @@ def run(lin, lay, M, kind, flags=0, **ep):
 CASES = [(1, 64, 128, 8), (2, 4096, 4096, 32), (7, 8, 8, 0), (8, 72, 136, 3), (9, 256, 1000, 16), (16, 4096, 512, 64),
          (17, 1032, 2744, 8), (31, 2056, 264, 128), (32, 512, 640, 15), (33, 520, 136, 24), (64, 4096, 1024, 64),
          (65, 264, 392, 0), (100, 1032, 520, 100), (128, 2048, 768, 32), (129, 272, 136, 31), (257, 1040, 1000, 64),
-         (300, 4104, 264, 128), (513, 528, 3000, 16)]
+         (300, 4104, 264, 128), (513, 528, 3000, 16),
+         # enough tiles for the kernel on pairs of CTAs, with a second CTA that has no channels,
+         # ragged tokens, channels and K, and very few channels
+         (4100, 1032, 520, 24), (2600, 264, 1000, 0), (9500, 72, 136, 8), (10000, 136, 8, 3), (1100, 4096, 2744, 128)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
@@ -76,7 +79,7 @@ def test_either_kernel_family_at_any_size(kind, path, M, K, N, r):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
-@pytest.mark.parametrize("M", [1, 5, 24, 70, 300])
+@pytest.mark.parametrize("M", [1, 5, 24, 70, 300, 4000])
 def test_every_term_and_the_ec_off(kind, M):
     from w4_gemm_error_b200.spear import SPEAR_EC_OFF
     lay = LayerRef(1024, 520, 20, seed=3)
@@ -100,7 +103,7 @@ def test_no_epilogue_is_the_forward_bit_for_bit(M, K, N, r):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
-@pytest.mark.parametrize("M", [1, 9, 31, 64, 200])
+@pytest.mark.parametrize("M", [1, 9, 31, 64, 200, 5000])
 def test_in_place_residual_and_multiplier(kind, M):
     lay = LayerRef(2048, 392, 16, seed=7)
     lin = lay.make(M)
@@ -113,7 +116,7 @@ def test_in_place_residual_and_multiplier(kind, M):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
-@pytest.mark.parametrize("M", [1, 12, 20, 40, 140])
+@pytest.mark.parametrize("M", [1, 12, 20, 40, 140, 4899])
 def test_rows_past_the_last_are_left_alone(kind, M):
     lay = LayerRef(512, 264, 8, seed=9)
     lin = lay.make(M)
@@ -123,7 +126,7 @@ def test_rows_past_the_last_are_left_alone(kind, M):
     assert (big[M:] == 5).all()
 
 
-@pytest.mark.parametrize("M", [1, 8, 16, 30, 33, 100, 300])
+@pytest.mark.parametrize("M", [1, 8, 16, 30, 33, 100, 300, 4997])
 def test_a_bad_token_stays_in_its_row(M):
     """NaN codes, NaN and infinite scales, infinite residuals reach only their own tokens."""
     lay = LayerRef(1024, 264, 16, seed=11)
@@ -151,7 +154,7 @@ def test_a_bad_token_stays_in_its_row(M):
     assert y[t, 3] == float("inf") and torch.isfinite(y[t, 4:]).all()
 
 
-@pytest.mark.parametrize("M", [1, 20, 64, 300])
+@pytest.mark.parametrize("M", [1, 20, 64, 300, 5000])
 def test_extreme_codes(M):
     """All codes at the largest magnitude, all at the smallest, zeros, one sign, every zero point."""
     lay = LayerRef(2048, 264, 8, seed=13)
@@ -186,7 +189,7 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])
-@pytest.mark.parametrize("M", [1, 24, 64, 300])
+@pytest.mark.parametrize("M", [1, 24, 64, 300, 5000])
 def test_captured_calls_on_two_handles(kind, M):
     """Two captured forwards of two handles, replayed with new data, in turn."""
     lays = [LayerRef(1032, 264, 8, seed=17), LayerRef(1024, 520, 32, seed=18)]
@@ -266,6 +269,33 @@ def test_many_calls_agree(kind, M, K, N, r):
         for i in range(3):
             bad += (got[i] != first[i]).sum()
     assert bad.item() == 0
+    assert all(lin.status() == 0 for lin in lins)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+def test_two_handles_on_two_streams(kind):
+    """Calls of all sizes of two layers, each on its own stream, at once."""
+    lays = [LayerRef(1032, 520, 24, seed=41), LayerRef(1024, 1000, 40, seed=42)]
+    lins = [lay.make(4200) for lay in lays]
+    streams = [torch.cuda.Stream() for _ in lays]
+    sizes = [4200, 1, 300, 16, 64, 12, 33, 200]
+    args = [[(bf16_x(lay, M),) if kind == "bf16" else q8_x(lay, M) for M in sizes] for lay in lays]
+    f = [lin.forward_ep if kind == "bf16" else lin.forward_q8 for lin in lins]
+    want = [[f[i](*a, act="relu") for a in args[i]] for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for k in range(len(sizes)):
+            for i in range(2):
+                got[i].append((k, f[i](*args[i][k], act="relu", stream=streams[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for k, y in got[i]:
+            assert torch.equal(y, want[i][k]), (i, sizes[k])
+    for i, lay in enumerate(lays):
+        a = args[i][0]
+        assert_layer(want[i][0], lay, a[0].double() if kind == "bf16" else a[0].double() * a[1].double()[:, None],
+                     "values", act="relu")
     assert all(lin.status() == 0 for lin in lins)
 
 

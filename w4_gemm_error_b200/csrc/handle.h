@@ -76,6 +76,17 @@ class DeviceGuard {
     bool ok_ = true;
 };
 
+// f's status; no exception (the host containers' allocations) crosses the C ABI.
+template <class F>
+int guarded(F f)
+{
+    try {
+        return f();
+    } catch (...) {
+        return SPEAR_ERR_NOMEM;
+    }
+}
+
 // Status of a CUDA runtime result (SPEAR_ERR_NOMEM for an allocation failure).
 int status_of(cudaError_t e);
 

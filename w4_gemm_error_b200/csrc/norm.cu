@@ -532,8 +532,10 @@ int spear_w4ec_rmsnorm(const void *x, const void *residual, const void *weight, 
     if (overlap(sum, n, y, n) || overlap(q, n / 2, weight, nw) || overlap(s, ns, weight, nw) ||
         overlap(q, n / 2, s, ns))
         return SPEAR_ERR_INVALID;
-    return spear::status_of(spear::launch_norm(x, residual, weight, eps, M, K, sum, y, q, s,
-                                               static_cast<cudaStream_t>(stream)));
+    return spear::guarded([&] {
+        return spear::status_of(spear::launch_norm(x, residual, weight, eps, M, K, sum, y, q, s,
+                                                   static_cast<cudaStream_t>(stream)));
+    });
 }
 
 int spear_w4ec_quantize_q8(const void *x, int64_t M, int64_t K, void *q, float *s, void *stream)
@@ -546,8 +548,10 @@ int spear_w4ec_quantize_q8(const void *x, int64_t M, int64_t K, void *q, float *
     if (!x || !q || !s || !aligned16(x) || !aligned16(q) || (reinterpret_cast<uintptr_t>(s) & 3u) != 0 ||
         overlap(x, 2 * n, q, n) || overlap(x, 2 * n, s, (size_t)M * 4) || overlap(q, n, s, (size_t)M * 4))
         return SPEAR_ERR_INVALID;
-    return spear::status_of(spear::launch_norm(x, nullptr, nullptr, 0.f, M, K, nullptr, nullptr, q, s,
-                                               static_cast<cudaStream_t>(stream)));
+    return spear::guarded([&] {
+        return spear::status_of(spear::launch_norm(x, nullptr, nullptr, 0.f, M, K, nullptr, nullptr, q, s,
+                                                   static_cast<cudaStream_t>(stream)));
+    });
 }
 
 }  // extern "C"

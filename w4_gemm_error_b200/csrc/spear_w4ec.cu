@@ -587,7 +587,8 @@ int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M
     DeviceGuard guard(h->device);
     if (!guard.ok())
         return SPEAR_ERR_CUDA;
-    return forward_ep_checked(h, x, nullptr, y, M, flags, static_cast<cudaStream_t>(stream), epi);
+    return guarded(
+        [&] { return forward_ep_checked(h, x, nullptr, y, M, flags, static_cast<cudaStream_t>(stream), epi); });
 }
 
 int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y, int64_t M,
@@ -611,7 +612,8 @@ int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, 
     DeviceGuard guard(h->device);
     if (!guard.ok())
         return SPEAR_ERR_CUDA;
-    return forward_ep_checked(h, xq, xs, y, M, flags, static_cast<cudaStream_t>(stream), epi);
+    return guarded(
+        [&] { return forward_ep_checked(h, xq, xs, y, M, flags, static_cast<cudaStream_t>(stream), epi); });
 }
 
 int spear_w4ec_forward_host(spear_w4ec *h, const void *x_host, void *y_host, int64_t M, uint32_t flags,

@@ -221,6 +221,63 @@ int run_ops(spear_w4ec_stack *s, const void *x, void *y, int64_t M, uint32_t fla
     return SPEAR_OK;
 }
 
+int set_op(spear_w4ec_stack *s, int32_t op, const spear_w4ec_stack_ext *ext)
+{
+    if (!s || op < 0 || op >= (int32_t)s->ops.size())
+        return SPEAR_ERR_INVALID;
+    const int32_t n_bufs = (int32_t)s->bufs.size();
+    const Packed &pk = s->ops[op].layer->pk;
+    if (ext) {
+        if (ext->act < SPEAR_ACT_NONE || ext->act > SPEAR_ACT_GELU_TANH || (ext->q8 != 0 && ext->q8 != 1) ||
+            !aligned16(ext->norm_weight) || !aligned16(ext->bias))
+            return SPEAR_ERR_INVALID;
+        if (ext->norm_weight && !(ext->norm_eps >= 0.0f && ext->norm_eps < 1e30f))
+            return SPEAR_ERR_INVALID;
+        // the width that each buffer has when the op runs
+        std::vector<int64_t> width(n_bufs, 0);
+        width[0] = s->in_width;
+        for (int32_t i = 0; i < op; ++i)
+            width[s->ops[i].out] = s->ops[i].layer->pk.N;
+        for (int32_t b : {ext->mul, ext->residual})
+            if (b != -1 && (b < 0 || b == 1 || b >= n_bufs || width[b] != pk.N))
+                return SPEAR_ERR_INVALID;
+    }
+    DeviceGuard guard(s->device);
+    if (!guard.ok())
+        return SPEAR_ERR_CUDA;
+    // scratch for the widest input of any op (an op may get its norm later)
+    cudaError_t e = cudaSuccess;
+    int64_t widest = 0;
+    for (const spear_w4ec_stack_op &o : s->ops)
+        widest = std::max(widest, o.layer->pk.K);
+    if (ext && ext->q8 && !s->q_buf) {
+        void *q = nullptr;
+        e = cudaMalloc(&q, (size_t)s->max_M * (size_t)widest);
+        if (e == cudaSuccess)
+            e = cudaMalloc(&s->q_scale, (size_t)s->max_M * sizeof(float));
+        if (e != cudaSuccess) {
+            cudaFree(q);
+            s->q_scale = nullptr;
+            cudaGetLastError();
+            return status_of(e);
+        }
+        s->q_buf = q;
+    }
+    if (ext && ext->norm_weight && !ext->q8 && !s->norm_buf) {
+        e = cudaMalloc(&s->norm_buf, (size_t)s->max_M * (size_t)widest * 2);
+        if (e != cudaSuccess) {
+            s->norm_buf = nullptr;
+            cudaGetLastError();
+            return status_of(e);
+        }
+    }
+    if (s->extras.empty())
+        s->extras.resize(s->ops.size());
+    s->extras[op].on = ext != nullptr;
+    s->extras[op].ext = ext ? *ext : spear_w4ec_stack_ext{};
+    return SPEAR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -347,59 +404,7 @@ int spear_w4ec_stack_forward_host(spear_w4ec_stack *s, const void *x_host, void 
 
 int spear_w4ec_stack_set_op(spear_w4ec_stack *s, int32_t op, const spear_w4ec_stack_ext *ext)
 {
-    if (!s || op < 0 || op >= (int32_t)s->ops.size())
-        return SPEAR_ERR_INVALID;
-    const int32_t n_bufs = (int32_t)s->bufs.size();
-    const Packed &pk = s->ops[op].layer->pk;
-    if (ext) {
-        if (ext->act < SPEAR_ACT_NONE || ext->act > SPEAR_ACT_GELU_TANH || (ext->q8 != 0 && ext->q8 != 1) ||
-            !aligned16(ext->norm_weight) || !aligned16(ext->bias))
-            return SPEAR_ERR_INVALID;
-        if (ext->norm_weight && !(ext->norm_eps >= 0.0f && ext->norm_eps < 1e30f))
-            return SPEAR_ERR_INVALID;
-        // the width that each buffer has when the op runs
-        std::vector<int64_t> width(n_bufs, 0);
-        width[0] = s->in_width;
-        for (int32_t i = 0; i < op; ++i)
-            width[s->ops[i].out] = s->ops[i].layer->pk.N;
-        for (int32_t b : {ext->mul, ext->residual})
-            if (b != -1 && (b < 0 || b == 1 || b >= n_bufs || width[b] != pk.N))
-                return SPEAR_ERR_INVALID;
-    }
-    DeviceGuard guard(s->device);
-    if (!guard.ok())
-        return SPEAR_ERR_CUDA;
-    // scratch for the widest input of any op (an op may get its norm later)
-    cudaError_t e = cudaSuccess;
-    int64_t widest = 0;
-    for (const spear_w4ec_stack_op &o : s->ops)
-        widest = std::max(widest, o.layer->pk.K);
-    if (ext && ext->q8 && !s->q_buf) {
-        void *q = nullptr;
-        e = cudaMalloc(&q, (size_t)s->max_M * (size_t)widest);
-        if (e == cudaSuccess)
-            e = cudaMalloc(&s->q_scale, (size_t)s->max_M * sizeof(float));
-        if (e != cudaSuccess) {
-            cudaFree(q);
-            s->q_scale = nullptr;
-            cudaGetLastError();
-            return status_of(e);
-        }
-        s->q_buf = q;
-    }
-    if (ext && ext->norm_weight && !ext->q8 && !s->norm_buf) {
-        e = cudaMalloc(&s->norm_buf, (size_t)s->max_M * (size_t)widest * 2);
-        if (e != cudaSuccess) {
-            s->norm_buf = nullptr;
-            cudaGetLastError();
-            return status_of(e);
-        }
-    }
-    if (s->extras.empty())
-        s->extras.resize(s->ops.size());
-    s->extras[op].on = ext != nullptr;
-    s->extras[op].ext = ext ? *ext : spear_w4ec_stack_ext{};
-    return SPEAR_OK;
+    return guarded([&] { return set_op(s, op, ext); });
 }
 
 int spear_w4ec_stack_buffer(const spear_w4ec_stack *s, int32_t index, void **ptr)
