@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p)
 // filled by bulk copies.  HBM bounds this case; with one CTA a row an SM's
 // loads pause while its CTAs reduce and store, and every CTA pays its launch
 // (2047 rows of 14336 quantised: 30 us, 2.9 TB/s).  Here the copies of the next
-// rows are in flight throughout, and the weights stay in registers.
+// rows are in flight throughout, and the weights stay in registers: 17 us,
+// 5.2 TB/s; 8192 rows of 4096 with residual to 8 bits 41.5 us, 5.7 TB/s.
 constexpr int kRing = 4;   // rows of the ring at most
 // CTAs an SM holds (of 512 threads with four vectors a thread, else of 256): as
 // many as the registers allow without spills, since a CTA's own chain (wait,

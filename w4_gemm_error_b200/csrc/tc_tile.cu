@@ -19,6 +19,12 @@
 // with mma.sync instead, the sums lagged six stages behind the product.)
 // Then all of them take the outputs of the CTA's 1/S of the tokens, two channels a
 // thread: the S partials, the epilogue, 4-byte stores of whole lines.
+// Measured in a chain of calls: 64 tokens of 14336 x 4096 in 8 bits 17.8 us
+// (24 with the Error Compensator and its prepass), 128 of 4096 x 14336 23.2 (26),
+// 333 of 2064 x 1000 9.6 (14), 33 of 256 x 256 5.0 (9).  About 590 cycles a stage;
+// of the 33000 of the first case 6000 pass until the first stage is there and 7000
+// from the last MMA to the end (partials, exchange, outputs), so that latency, not
+// the 4.6 us of its HBM bytes, bounds it.
 // Every wait is bounded (about a second); one that runs out sets the handle's
 // status word and the kernel winds down.
 #include <algorithm>
