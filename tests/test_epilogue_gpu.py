@@ -299,6 +299,44 @@ def test_two_handles_on_two_streams(kind):
     assert all(lin.status() == 0 for lin in lins)
 
 
+@pytest.mark.parametrize("r", [0, 8])
+@pytest.mark.parametrize("M", [1, 24, 300, 2600])
+def test_operands_from_the_call_before(M, r):
+    """Bias, multiplier and residual that the call right before on the stream writes."""
+    a, b = LayerRef(14336, 1000, 0, seed=41), LayerRef(264, 1000, r, seed=42)
+    la, lb = a.make(max(M, 1)), b.make(M)
+    x = bf16_x(b, M)
+    first = [bf16_x(a, 1) for _ in range(8)]
+    rows = [bf16_x(a, M) for _ in range(2)]
+    want = []
+    for v in first:
+        bias = la.forward_ep(v)[0].clone()
+        torch.cuda.synchronize()
+        want.append(lb.forward_ep(x, bias=bias))
+        torch.cuda.synchronize()
+    bias, got = torch.zeros(1, 1000, dtype=torch.bfloat16, device="cuda"), []
+    torch.cuda.synchronize()
+    for v in first:
+        la.forward_ep(v, out=bias)
+        got.append(lb.forward_ep(x, bias=bias[0]))
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+    for name in ("mul", "residual"):
+        want = []
+        for v in rows:
+            o = la.forward_ep(v).clone()
+            torch.cuda.synchronize()
+            want.append(lb.forward_ep(x, **{name: o}))
+            torch.cuda.synchronize()
+        buf, got = torch.zeros(M, 1000, dtype=torch.bfloat16, device="cuda"), []
+        torch.cuda.synchronize()
+        for v in rows:
+            la.forward_ep(v, out=buf)
+            got.append(lb.forward_ep(x, **{name: buf}))
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
 def test_results_repeat_bit_for_bit():
     lay = LayerRef(4096, 520, 64, seed=21)
     for M in (1, 16, 24, 64, 300):

@@ -415,6 +415,8 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         const bool storer = q == 0 && lane == 0;
         uint32_t g = 0;
         int lt = 0, stores = 0;
+        if (!p.v_ready)
+            pdl_wait();   // the bias may come from an earlier kernel (early start: the prepass waited for it)
         // a wait that gives up ends this warp's waits and stores, but not its
         // loops: the warps of a set meet in a barrier at every slot
         bool ok = true;
