@@ -411,7 +411,9 @@ typedef struct spear_w4ec_stack_ext {
  * width N of this one (SPEAR_ERR_INVALID otherwise).  Ops in a row that read one
  * buffer with one norm share its result.  Allocates scratch for the stack's
  * normed or 8-bit activations at the first op that needs it.  An op that was set
- * runs as spear_w4ec_forward_ep / _forward_q8 (same flags); a stack with one
+ * runs as spear_w4ec_forward_ep / _forward_q8 (same flags).  The stack's y may
+ * then be x itself, unless the last op reads x as it is; what else of x or of the
+ * last op's bias overlaps y is SPEAR_ERR_INVALID.  A stack with such an op
  * does not run as SPEAR_STACK_PERSISTENT (SPEAR_ERR_UNSUPPORTED). */
 int spear_w4ec_stack_set_op(spear_w4ec_stack *s, int32_t op, const spear_w4ec_stack_ext *ext);
 

@@ -414,3 +414,14 @@ def test_refusals():
     assert lin.forward_ep(x[:0]).shape == (0, lay.N)
     assert lin.forward_q8(q[:0], s[:0]).shape == (0, lay.N)
     assert lin.status() == 0
+
+
+def test_an_input_on_another_device_is_refused():
+    lay = LayerRef(256, 264, 8, seed=26)
+    lin = lay.make(4)
+    x, (q, s) = bf16_x(lay, 4), q8_x(lay, 4)
+    lin.device = torch.device("cuda", x.get_device() + 1)
+    with pytest.raises(ValueError):
+        lin.forward_ep(x)
+    with pytest.raises(ValueError):
+        lin.forward_q8(q, s)

@@ -130,6 +130,44 @@ def test_a_buffer_written_again_is_normed_again():
     assert_layer(st.buffer(2, 3), lay, b3.double(), "in place", residual=first)
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("M", [1, 30, 200])
+def test_output_in_the_place_of_the_input(q8, M):
+    """x is normed by the first op and added by the second, y written by the last."""
+    blk = Block(M, q8)
+    x = blk.lays["q"].normal(M, H).bfloat16()
+    want, was = blk.stack(x), x.clone()
+    assert blk.stack(x, out=x) is x
+    assert torch.equal(x, want)
+    blk.check(was, x)
+
+
+def test_output_over_what_the_last_op_reads():
+    from w4_gemm_error_b200 import spear
+    lay = LayerRef(H, H, 8, seed=37)
+    lin = lay.make(8)
+    st = spear.W4ECStack([(lin, 0, 2, 1), (lin, 0, 1, 1)], 8)
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    flat = lay.normal(6 * H).bfloat16()
+    x, shifted = flat[:4 * H].view(4, H), flat[8:8 + 4 * H].view(4, H)
+
+    def refused(out):
+        with pytest.raises(spear.SpearError) as e:
+            st(x, out=out)
+        assert e.value.status == spear.SPEAR_ERR_INVALID
+
+    st.set_op(1, act="relu")                # the layer reads x itself
+    refused(x)
+    refused(shifted)
+    st.set_op(1, residual=0, q8=True)       # x is quantised before, and added element by element
+    refused(shifted)
+    st.set_op(1, norm=w, bias=flat[2 * H:3 * H])
+    refused(x)                              # the bias lies in y
+    st.set_op(1, norm=w, residual=0)
+    want = st(x)
+    assert torch.equal(st(x, out=x), want)
+
+
 def test_refusals():
     from w4_gemm_error_b200 import spear
     blk = Block(8, False)

@@ -172,10 +172,33 @@ int run_persistent(spear_w4ec_stack *s, const void *x, void *y, int64_t M, uint3
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether the last op, if it was set, could read x or a bias after it has begun
+// to write y over it.  (y in the place of x itself is fine for an epilogue, which
+// reads each element before it writes it, and for an input that is normed or
+// quantised first.)
+bool clashes(const spear_w4ec_stack *s, const void *x, const void *y, int64_t M)
+{
+    if (s->extras.empty() || !s->extras.back().on)
+        return false;
+    const spear_w4ec_stack_ext &e = s->extras.back().ext;
+    const size_t nx = (size_t)M * (size_t)s->in_width * 2, ny = (size_t)M * (size_t)s->out_width * 2;
+    auto meet = [&](const void *a, size_t na) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(y);
+        return a && p < q + ny && q < p + na;
+    };
+    if (meet(e.bias, (size_t)s->out_width * 2))
+        return true;
+    if (!meet(x, nx))
+        return false;
+    return (s->ops.back().in == 0 && !e.norm_weight && !e.q8) || (x != y && (e.mul == 0 || e.residual == 0));
+}
+
 int run_ops(spear_w4ec_stack *s, const void *x, void *y, int64_t M, uint32_t flags, cudaStream_t st)
 {
     if (flags & SPEAR_STACK_PERSISTENT)
         return run_persistent(s, x, y, M, flags & ~(uint32_t)SPEAR_STACK_PERSISTENT, st);
+    if (clashes(s, x, y, M))
+        return SPEAR_ERR_INVALID;
     // the op whose normed (bf16) and whose 8-bit input the scratch holds (-1: none)
     int held[2] = {-1, -1};
     for (size_t i = 0; i < s->ops.size(); ++i) {

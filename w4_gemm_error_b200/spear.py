@@ -515,6 +515,8 @@ class W4ECLinear:
 
     def _epilogue(self, M, act, bias, mul, residual, dev):
         """The spear_w4ec_epilogue of a call, or None for one that does nothing."""
+        if dev != self.device.index:
+            raise ValueError(f"the layer is on {self.device}, its input on cuda:{dev}")
         try:
             code = ACTIVATIONS[act]
         except (KeyError, TypeError):
