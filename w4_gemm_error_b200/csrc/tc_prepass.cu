@@ -11,10 +11,15 @@
 // A cluster of S CTAs takes 128 tokens; CTA q the 64-k blocks q, q + S, ...
 // The tokens are the 128 rows (TMEM lanes) of the MMA and the rows of G its N.
 // One CTA a tile leaves most SMs idle (16 of them work at 2048 tokens of K = 4096,
-// 29 us alone and cold; S = 8 there: 14 us).  The loop runs at about 600 cycles a
-// 64-k block; at few tokens the exchange and what surrounds it take as long.  e4m3 activations are made bf16 on
-// their way from the copied tile to the MMA's (exact), and sixteen rows of ones
-// behind those of G make X_t one more column of D.  The S partial
+// 29 us alone and cold; S = 8 there: 14 us).  The loop runs at about 540 cycles a
+// 64-k block (630 with the copies issued from a single lane's branch); at few
+// tokens the exchange and what surrounds it take as long.
+// (As first CTAs of tc_tile.cu's grid, their partials exchanged through global
+// memory, the same work took longer by three more trips to L2: 33 tokens of
+// 256 x 256 in 12.5 us instead of 9.2.)
+// e4m3 activations are made bf16 on their way from the copied tile to the MMA's
+// (exact), and sixteen rows of ones behind those of G make X_t one more column of
+// D; a NaN code is a number here, but the product beside it is NaN.  The S partial
 // accumulators meet in shared memory: CTA q sums its 128 / S tokens over the
 // cluster in rank order (run-to-run identical), forms the gate and writes v.
 #include <algorithm>
@@ -142,25 +147,30 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 
     const int q = warp & 3, row = 32 * q + lane;   // warps 2 and up: TMEM lane = token of the tile
     if (warp == 0) {
-        if (lane == 0) {
-            int issued = 0;
-            for (int i = 0; i < nkb; ++i, ++issued) {
-                const uint32_t slot = i % kStages, phase = (i / kStages) & 1;
-                if (!mbar_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status))
-                    break;
-                const uint32_t sb = base + slot * sbytes, full = full0 + 8 * slot;
-                const int k = (rank + i * S) * 64;
+        const bool elected = elect_one();
+        uint32_t slot = 0, phase = 0;
+        int issued = 0;
+        for (int i = 0; i < nkb; ++i, ++issued) {
+            if (!warp_wait(empty0 + 8 * slot, phase ^ 1, &abort_flag, p.status))
+                break;
+            const uint32_t sb = base + slot * sbytes, full = full0 + 8 * slot;
+            const int k = (rank + i * S) * 64;
+            if (elected) {
                 mbar_expect_tx(full, (FORM == kQ8 ? xin_bytes<FORM>() : kTok * 128) + g_bytes);
                 tma_load_2d(FORM == kQ8 ? sb + kXin : sb, &tm_x, k, t0, full);
                 if (ec)
                     tma_load_2d(sb + o_g, &tm_g, k, 0, full);
             }
-            if (abort_flag)
-                for (int j = 0; j < kStages && j < issued; ++j) {
-                    const int i = issued - 1 - j;
-                    mbar_wait_final(full0 + 8 * (i % kStages), (i / kStages) & 1);
-                }
+            if ((int)++slot == kStages) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
+        if (abort_flag)
+            for (int j = 0; j < kStages && j < issued; ++j) {
+                const int i = issued - 1 - j;
+                mbar_wait_final(full0 + 8 * (i % kStages), (i / kStages) & 1);
+            }
     } else if (warp == 1) {
         const bool elected = elect_one();
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(ncol >> 3) << 17) |
@@ -211,10 +221,8 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                 const uint32_t words[4] = {w.x, w.y, w.z, w.w};
                 uint32_t o[8];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    o[2 * h] = f16x2_to_bf16x2(e4m3x2_to_f16x2((uint16_t)words[h]));
-                    o[2 * h + 1] = f16x2_to_bf16x2(e4m3x2_to_f16x2((uint16_t)(words[h] >> 16)));
-                }
+                for (int h = 0; h < 4; ++h)
+                    e4m3x4_to_bf16(words[h], o[2 * h], o[2 * h + 1]);
                 *reinterpret_cast<uint4 *>(dst + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4 *>(dst + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
