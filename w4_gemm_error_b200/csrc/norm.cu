@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p)
 // 5.2 TB/s; 8192 rows of 4096 with residual to 8 bits 41.5 us, 5.7 TB/s.
 constexpr int kRing = 4;   // rows of the ring at most
 // CTAs an SM holds (of 512 threads with four vectors a thread, else of 256): as
-// many as the registers allow without spills, since a CTA's own chain (wait,
+// many as the registers allow (nearly without spills), since a CTA's own chain (wait,
 // statistics, barrier, outputs) is latency and only other CTAs fill it.
 __host__ __device__ constexpr int rows_per_sm(int nv, bool norm) { return nv == 4 ? (norm ? 2 : 3) : (norm ? 5 : 6); }
 
