@@ -374,6 +374,14 @@ def _dev(t, dtype, shape, name, index):
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
 
 
+def _out(t, dtype, shape, name, x):
+    """(tensor, address) of an output: the caller's, checked, or a new one beside x."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=x.device)
+        return t, t.data_ptr()
+    return t, _dev(t, dtype, shape, name, x.get_device())
+
+
 def _cuda_rows(x, name):
     """(M, K, device index) of a CUDA tensor [M, K]."""
     try:
@@ -429,15 +437,12 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
     y = q = s = h = py = pq = ps = ph = pr = None
     if residual is not None:
         pr = _dev(residual, tb, rows, "residual", dev)
-        h = torch.empty_like(x) if out_sum is None else out_sum
-        ph = _dev(h, tb, rows, "out_sum", dev)
+        h, ph = _out(out_sum, tb, rows, "out_sum", x)
     if bf16:
-        y = torch.empty_like(x) if out is None else out
-        py = _dev(y, tb, rows, "out", dev)
+        y, py = _out(out, tb, rows, "out", x)
     if q8:
-        q = torch.empty(rows, dtype=torch.float8_e4m3fn, device=x.device) if out_q is None else out_q
-        s = torch.empty(M, dtype=torch.float32, device=x.device) if out_s is None else out_s
-        pq, ps = _dev(q, torch.float8_e4m3fn, rows, "out_q", dev), _dev(s, torch.float32, (M,), "out_s", dev)
+        q, pq = _out(out_q, torch.float8_e4m3fn, rows, "out_q", x)
+        s, ps = _out(out_s, torch.float32, (M,), "out_s", x)
     _call_on(dev, _lib.spear_w4ec_rmsnorm, "spear_w4ec_rmsnorm", px, pr, pw, eps, M, K, ph, py, pq, ps,
              _stream_on(stream, dev))
     return y, q, s, h
@@ -450,9 +455,8 @@ def quantize_q8(x: torch.Tensor, *, out_q: torch.Tensor | None = None, out_s: to
     M, K, dev = _cuda_rows(x, "x")
     rows = (M, K)
     px = _dev(x, torch.bfloat16, rows, "x", dev)
-    q = torch.empty(rows, dtype=torch.float8_e4m3fn, device=x.device) if out_q is None else out_q
-    s = torch.empty(M, dtype=torch.float32, device=x.device) if out_s is None else out_s
-    pq, ps = _dev(q, torch.float8_e4m3fn, rows, "out_q", dev), _dev(s, torch.float32, (M,), "out_s", dev)
+    q, pq = _out(out_q, torch.float8_e4m3fn, rows, "out_q", x)
+    s, ps = _out(out_s, torch.float32, (M,), "out_s", x)
     _call_on(dev, _lib.spear_w4ec_quantize_q8, "spear_w4ec_quantize_q8", px, M, K, pq, ps, _stream_on(stream, dev))
     return q, s
 
@@ -537,8 +541,7 @@ class W4ECLinear:
         and residual bf16 [M, N] (each may be ``out`` itself)."""
         M, _, dev = _cuda_rows(x, "x")
         px = _dev(x, torch.bfloat16, (M, self.K), "x", dev)
-        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device) if out is None else out
-        py = _dev(y, torch.bfloat16, (M, self.N), "out", dev)
+        y, py = _out(out, torch.bfloat16, (M, self.N), "out", x)
         ep = self._epilogue(M, act, bias, mul, residual, dev)
         rc = _lib.spear_w4ec_forward_ep(self.h, px, py, M, ep, flags, _stream_on(stream, dev))
         if rc:
@@ -553,8 +556,7 @@ class W4ECLinear:
         M, _, dev = _cuda_rows(xq, "xq")
         px = _dev(xq, torch.float8_e4m3fn, (M, self.K), "xq", dev)
         ps = _dev(xs, torch.float32, (M,), "xs", dev)
-        y = torch.empty((M, self.N), dtype=torch.bfloat16, device=xq.device) if out is None else out
-        py = _dev(y, torch.bfloat16, (M, self.N), "out", dev)
+        y, py = _out(out, torch.bfloat16, (M, self.N), "out", xq)
         ep = self._epilogue(M, act, bias, mul, residual, dev)
         rc = _lib.spear_w4ec_forward_q8(self.h, px, ps, py, M, ep, flags, _stream_on(stream, dev))
         if rc:
