@@ -48,7 +48,9 @@ CASES = [(1, 64, 128, 8), (2, 4096, 4096, 32), (7, 8, 8, 0), (8, 72, 136, 3), (9
          (300, 4104, 264, 128), (513, 528, 3000, 16),
          # enough tiles for the kernel on pairs of CTAs, with a second CTA that has no channels,
          # ragged tokens, channels and K, and very few channels
-         (4100, 1032, 520, 24), (2600, 264, 1000, 0), (9500, 72, 136, 8), (10000, 136, 8, 3), (1100, 4096, 2744, 128)]
+         (4100, 1032, 520, 24), (2600, 264, 1000, 0), (9500, 72, 136, 8), (10000, 136, 8, 3), (1100, 4096, 2744, 128),
+         # the same kernel with fewer tokens than one tile of it
+         (40, 520, 9480, 24), (100, 264, 9608, 8), (128, 136, 19000, 0), (65, 72, 19200, 128)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q8"])

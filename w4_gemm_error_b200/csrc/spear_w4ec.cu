@@ -175,7 +175,7 @@ int run_tc_form(const spear_w4ec *h, const void *x, int64_t ldx, void *y, int64_
         const int bits = kStatusTimeout;
         return from_cuda(cudaMemcpyAsync(h->status, &bits, sizeof(int), cudaMemcpyHostToDevice, st));
     }
-    const bool pair = tc_use_pair(pk, M, h->num_sms);
+    const bool pair = tc_use_pair(pk, M, ec, form, h->num_sms);
     unsigned *ready = ec ? h->vready : nullptr;
     unsigned expected = 0;
     cudaError_t e = cudaSuccess;

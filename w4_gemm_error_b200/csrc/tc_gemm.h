@@ -50,7 +50,9 @@ const CUtensorMap *tc_map_bt(const TcWork &w);   // (of a packed layer with an E
 // `ec`, rowc in form kQ8 (xs: its scales).  Rows of x are ldx elements apart.
 // `ready` (may be null) is counted *expected times in all, once per CTA when
 // what it writes is there.
-int tc_prepass2_split(const Packed &pk, int64_t M, int num_sms);   // CTAs per 128 tokens
+// SMs to leave free for a kernel that is to start beside it: its CTAs and a
+// quarter more, since whole clusters of up to 8 need their places.
+int64_t tc_prepass2_room(const Packed &pk, int64_t M, int num_sms);
 cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, const float *xs, int64_t M, bool ec,
                                float *v, float *rowc, int form, const CUtensorMap *g, int *status, cudaStream_t st,
                                int num_sms, unsigned *ready, unsigned *expected);
@@ -58,7 +60,7 @@ cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, con
 // The product and epilogue: pairs of CTAs on 256 x 256 tiles (tc_pair.cu, which
 // reads rowc), or one CTA on 128 x up to 128 with K split over a cluster
 // (tc_tile.cu, which sums the codes itself).  v_ready, v_expected: as launch_tc.
-bool tc_use_pair(const Packed &pk, int64_t M, int num_sms);
+bool tc_use_pair(const Packed &pk, int64_t M, bool ec, int form, int num_sms);
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,
                            const CUtensorMap *bt, int *status, cudaStream_t st, int num_sms, unsigned *v_ready,
                            unsigned v_expected, int form, const Epilogue &epi, int64_t ldx, const float *rowc);

@@ -1,6 +1,6 @@
 // W4 GEMM of many tokens with an epilogue, on pairs of CTAs (tcgen05,
 // cta_group::2): the forms kEpi (bf16 activations) and kQ8 (e4m3) of the
-// forward pass from 129 tokens on.
+// forward pass where there are many tiles (tc_use_pair).
 //
 //   D[n, t] = sum_k a[n,k] x[t,k] + sum_j (B[j,n] / e[n]) v[t,j]
 //   form kEpi:  a = q - z,     Y = e[n] D                       (bf16 MMAs)
@@ -561,13 +561,30 @@ using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUte
 
 }  // namespace
 
-// Whether the forms with an epilogue take these kernels' 256 x 256 tiles: they
-// read half as much per product as the 128 x 128 ones of tc_tile.cu, but leave
-// SMs idle below half a machine of pairs.
-bool tc_use_pair(const Packed &pk, int64_t M, int num_sms)
+// Whether the forms with an epilogue take these kernels' 256 x 256 tiles or the
+// 128 x 128 ones of tc_tile.cu.  Those read twice as much per product and a stage
+// takes longer, but they can split K: they win while they can split it at least
+// in two (of equal work the pairs finish first).  Measured in us, tile against
+// pair, bf16 / 8 bits:
+//   4096 x 4096, r 32    256 tokens (K in 2)  20.5 / 18.4 against 30.5 / 22.2
+//                        512 tokens (whole)   36.5 / 32.4 against 31.8 / 23.0
+//   14336 x 4096, r 64   256 tokens (K in 2)  47.5 / 36.7 against 76.9 / 47.8
+//                        512 tokens (whole)   92.4 / 73.9 against 80.4 / 49.5
+//   4096 x 14336, r 64   128 tokens (whole)   32.4 / 27.0 against 30.7 / 21.3
+//                         64 tokens (whole)   26.7 / 22.3 against 28.9 / 19.8
+//   8192 x 512, r 64    1024 tokens (K in 2)  31.2 / 24.9 against 49.3 / 32.2
+//                       1536 tokens (whole)   52.4 / 40.2 against 51.1 / 33.1
+//   2048 x 512, no EC   4096 tokens (whole)   21.6 / 17.5 against 18.5 / 22.2
+// The last one, in 8 bits, needs a prepass (of the code sums) for the pairs alone:
+// there they are taken from more tiles than SMs on.
+bool tc_use_pair(const Packed &pk, int64_t M, bool ec, int form, int num_sms)
 {
-    const int64_t pairs = (M + BN - 1) / BN * ((pk.Np + 2 * BM - 1) / (2 * BM));
-    return M > 128 && 4 * pairs >= num_sms;
+    if (M <= (form == kQ8 ? 32 : 64))
+        return false;
+    const int64_t tok = M <= 64 ? 64 : 128, tiles = (M + tok - 1) / tok * (pk.Np / 128);
+    if (form == kQ8 && !ec)
+        return tiles > num_sms;
+    return 2 * tiles + (ec ? tc_prepass2_room(pk, M, num_sms) : 0) > num_sms;
 }
 
 cudaError_t launch_tc_pair(const Packed &pk, const void *x, void *y, int64_t M, const float *v, bool ec,

@@ -321,8 +321,6 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         cluster_sync();   // no CTA leaves while another reads its partial
 }
 
-}  // namespace
-
 // As many CTAs a tile as keep one SM each, up to the portable cluster of 8.
 int tc_prepass2_split(const Packed &pk, int64_t M, int num_sms)
 {
@@ -331,6 +329,13 @@ int tc_prepass2_split(const Packed &pk, int64_t M, int num_sms)
     while (S < kMaxCluster && 2 * S <= (int)(pk.Kp / 64) && tiles * 2 * S <= num_sms)
         S *= 2;
     return S;
+}
+
+}  // namespace
+
+int64_t tc_prepass2_room(const Packed &pk, int64_t M, int num_sms)
+{
+    return (M + kTok - 1) / kTok * tc_prepass2_split(pk, M, num_sms) * 5 / 4;
 }
 
 cudaError_t launch_tc_prepass2(const Packed &pk, const void *x, int64_t ldx, const float *xs, int64_t M, bool ec,

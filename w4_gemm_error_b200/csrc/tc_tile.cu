@@ -406,11 +406,10 @@ cudaError_t launch_tc_tile(const Packed &pk, const void *x, void *y, int64_t M, 
     if (e != cudaSuccess)
         return e;
     // K over as many CTAs a tile as are all resident at once, at least four
-    // stages a CTA, beside the prepass with the EC (whose clusters of up to 8
-    // the count of whole clusters may not fit around: a quarter more; clusters
-    // that have to wait for it make the two run one after the other, 31 us
-    // instead of 24 at 64 tokens of a 14336x4096 layer)
-    const int64_t beside = use_ec ? (M + 127) / 128 * tc_prepass2_split(pk, M, num_sms) * 5 / 4 : 0;
+    // stages a CTA, beside the prepass with the EC (clusters that have to wait for
+    // it make the two run one after the other, 31 us instead of 24 at 64 tokens
+    // of a 14336x4096 layer)
+    const int64_t beside = use_ec ? tc_prepass2_room(pk, M, num_sms) : 0;
     int S = (int)std::min<int64_t>({kMaxSplit, std::max(1, p.n_main / 4), std::max<int64_t>(1, num_sms / units)});
     while (S > 1 && !grid_is_one_wave(reinterpret_cast<const void *>(fn), THREADS, smem, S, units * S + beside, num_sms))
         --S;
