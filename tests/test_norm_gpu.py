@@ -21,9 +21,11 @@ def rows(M, K, seed=0, std=1.0):
 
 SHAPES = [(1, 8), (1, 4096), (3, 1), (2, 7), (5, 31), (4, 66), (37, 2050), (9, 2048), (2, 4104), (33, 1032),
           (3, 14336), (2, 16384), (2, 16390), (1, 32768), (2, 40000), (1, 33001), (300, 256), (1, 131072),
-          # many rows: the kernel that streams them, with one to four vectors a thread and one warp upwards
+          # many rows, with one to four vectors a thread and one warp upwards
           (700, 8), (1500, 64), (999, 264), (1201, 1032), (2049, 2048), (650, 4104), (800, 10000), (601, 14336),
-          (1200, 16384), (593, 2050)]
+          (1200, 16384), (593, 2050),
+          # many short rows: a warp each
+          (2371, 1), (2400, 8), (2371, 50), (3001, 33), (2369, 127), (4000, 512), (2999, 1024), (2500, 254)]
 
 
 @pytest.mark.parametrize("M,K", SHAPES)
@@ -113,6 +115,23 @@ def test_rows_past_the_last_are_left_alone(M):
             out_sum=big["h"][:M])
     assert (big["y"][M:] == 7).all() and (big["h"][M:] == 7).all() and (s[M:] == 7).all()
     assert (q.view(torch.uint8)[M:] == 7).all()
+
+
+@pytest.mark.parametrize("M,K", [(2371, 512), (2374, 65)])
+def test_short_rows_in_place_and_past_the_last(M, K):
+    from w4_gemm_error_b200.spear import quantize_q8, rmsnorm
+    x, w, res = rows(M, K, 1), rows(1, K, 2)[0], rows(M, K, 3)
+    y, _, _, h = rmsnorm(x, w, EPS, res)
+    buf = torch.full((M + 9, K), 7, dtype=torch.bfloat16, device="cuda")
+    buf[:M] = x
+    r = res.clone()
+    rmsnorm(buf[:M], w, EPS, r, out=buf[:M], out_sum=r)
+    assert torch.equal(buf[:M], y) and torch.equal(r, h) and (buf[M:] == 7).all()
+    q = torch.full((M + 9, K), 7, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s = torch.full((M + 9,), 7.0, device="cuda")
+    quantize_q8(x, out_q=q[:M], out_s=s[:M])
+    assert_codes(q[:M], s[:M], x.double(), 0.0, "q")
+    assert (q.view(torch.uint8)[M:] == 7).all() and (s[M:] == 7).all()
 
 
 def test_offsets_past_32_bits():

@@ -18,10 +18,7 @@
 // All sums are fp32; v is rounded once to each output type.
 #include <cuda_runtime.h>
 
-#include <algorithm>
-
 #include "async_utils.cuh"
-#include "kernels.h"
 #include "handle.h"
 #include "norm.h"
 #include "spear_w4ec.h"
@@ -30,6 +27,7 @@ namespace spear {
 namespace {
 
 constexpr float kE4m3Max = 448.0f;
+constexpr int kWarpRows = 8;   // rows of a CTA with one warp a row
 constexpr float kAmaxFloor = 7.888609052210118e-31f;   // 2^-100: 448 / a stays finite
 
 struct NormParams {
@@ -41,7 +39,7 @@ struct NormParams {
     uint16_t *y;                // null: none
     uint8_t *q;                 // null: none
     float *s;
-    int64_t K;
+    int64_t M, K;
 };
 
 // VEC consecutive bf16 elements (8, 2 or 1) as packed pairs.
@@ -112,17 +110,17 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[VEC])
     }
 }
 
-// Sum and maximum over the CTA, the same in every thread.  The maximum is of
+// Sum and maximum over the nw warps of a row, the same in every thread.  The maximum is of
 // non-negative values (or NaN) as bit patterns: unsigned order keeps a NaN,
 // which is above every number, so that a bad row is seen.
 struct Reduce {
     float sum[32];
     uint32_t top[32];
 };
-__device__ __forceinline__ void block_reduce(float &sum, float &most, Reduce &s)
+__device__ __forceinline__ void block_reduce(float &sum, float &most, Reduce &s, int nw)
 {
     uint32_t top = __float_as_uint(most) & 0x7FFFFFFFu;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (int)(blockDim.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -216,19 +214,27 @@ __device__ __forceinline__ void emit(const NormParams &p, int64_t at, const Vec<
     }
 }
 
-// ---- one CTA a row: few rows, rows that are no multiple of 8 elements, or
-// rows too long for the pipelined kernel below.
-// NV vectors of VEC elements a thread; NV = 0: the row is longer than the
-// registers hold and is read again for the outputs (a sum that was stored is
-// read back, since x or the residual may be the same memory).
-template <int VEC, int NV, bool NORM>
-__global__ void __launch_bounds__(1024) norm_kernel(NormParams p)
+// One CTA a row, or (WARP) one warp a row where a warp holds it: short rows cost
+// a CTA's launch each otherwise (8192 rows of 512 quantised: 3.6 us instead of 8.9).
+// HBM bounds many rows (8192 rows of 4096 with residual to 8 bits: 42.5 us, 5.5
+// TB/s; 2047 of 14336 quantised: 14.8 us, 5.9 TB/s): enough CTAs an SM are resident
+// that others load while one reduces and stores.  (Persistent CTAs with a ring of
+// rows filled by bulk copies took 43.2 and 16.8 us.)
+// NV vectors of VEC elements a thread;
+// NV = 0: the row is longer than the registers hold and is read again for the
+// outputs (a sum that was stored is read back, since x or the residual may be the
+// same memory).
+template <int VEC, int NV, bool NORM, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_kernel(NormParams p)
 {
     __shared__ Reduce s_red;
     pdl_launch_dependents();
     pdl_wait();   // every operand may come from an earlier kernel in the stream
-    const int64_t at = (int64_t)blockIdx.x * p.K;
-    const int T = (int)blockDim.x, tid = (int)threadIdx.x;
+    const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP && row >= p.M)
+        return;
+    const int64_t at = row * p.K;
+    const int T = WARP ? 32 : (int)blockDim.x, tid = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int64_t nvec = p.K / VEC;
     const bool q8 = p.q != nullptr;
     constexpr int kN = NV > 0 ? NV : 1;
@@ -269,10 +275,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p)
             count<VEC, NORM>(h[0], w[0], q8, sum, top);
         }
     }
-    block_reduce(sum, top, s_red);
+    block_reduce(sum, top, s_red, WARP ? 1 : T >> 5);
     const Factors f = factors<NORM>(p, sum, top);
     if (q8 && tid == 0)
-        p.s[blockIdx.x] = f.a / kE4m3Max;
+        p.s[row] = f.a / kE4m3Max;
     if constexpr (NV > 0) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -290,132 +296,21 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p)
     }
 }
 
-// ---- many rows: persistent CTAs, each with a ring of rows in shared memory
-// filled by bulk copies.  HBM bounds this case; with one CTA a row an SM's
-// loads pause while its CTAs reduce and store, and every CTA pays its launch
-// (2047 rows of 14336 quantised: 30 us, 2.9 TB/s).  Here the copies of the next
-// rows are in flight throughout, and the weights stay in registers: 17 us,
-// 5.2 TB/s; 8192 rows of 4096 with residual to 8 bits 41.5 us, 5.7 TB/s.
-constexpr int kRing = 4;   // rows of the ring at most
-// CTAs an SM holds (of 512 threads with four vectors a thread, else of 256): as
-// many as the registers allow (nearly without spills), since a CTA's own chain (wait,
-// statistics, barrier, outputs) is latency and only other CTAs fill it.
-__host__ __device__ constexpr int rows_per_sm(int nv, bool norm) { return nv == 4 ? (norm ? 2 : 3) : (norm ? 5 : 6); }
-
-template <int NV, bool NORM>
-__global__ void __launch_bounds__(NV == 4 ? 512 : 256, rows_per_sm(NV, NORM)) norm_rows_kernel(NormParams p, int64_t M, int ring)
-{
-    extern __shared__ __align__(128) uint8_t rows[];   // [ring][x row, residual row]
-    __shared__ Reduce s_red[2];
-    __shared__ __align__(8) uint64_t bars[kRing];
-    const int T = (int)blockDim.x, tid = (int)threadIdx.x;
-    const int nvec = (int)(p.K / 8);
-    const uint32_t row_bytes = (uint32_t)p.K * 2, stage_bytes = row_bytes * (p.residual ? 2 : 1);
-    const bool q8 = p.q != nullptr;
-    if (tid == 0) {
-        for (int s = 0; s < ring; ++s)
-            mbar_init(smem_addr(&bars[s]), 1);
-        fence_mbarrier_init_cluster();
-    }
-    __syncthreads();
-    pdl_launch_dependents();
-    pdl_wait();   // every operand may come from an earlier kernel in the stream
-    auto request = [&](int64_t t, int s) {
-        const uint32_t bar = smem_addr(&bars[s]), dst = smem_addr(rows) + (uint32_t)s * stage_bytes;
-        mbar_expect_tx(bar, stage_bytes);
-        bulk_load(dst, p.x + t * p.K, row_bytes, bar);
-        if (p.residual)
-            bulk_load(dst + row_bytes, p.residual + t * p.K, row_bytes, bar);
-    };
-    if (tid == 0)
-        for (int s = 0; s < ring; ++s)
-            if (blockIdx.x + (int64_t)s * gridDim.x < M)
-                request(blockIdx.x + (int64_t)s * gridDim.x, s);
-    Vec<8> w[NV] = {};
-    if (NORM) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (tid + j * T < nvec)
-                w[j] = load_vec<8>(p.w + (int64_t)(tid + j * T) * 8);
-    }
-    int s = 0, prev = -1, round = 0;
-    uint32_t phase = 0;
-    for (int64_t t = blockIdx.x; t < M; t += gridDim.x, ++round) {
-        // a copy that never lands (bounded wait) leaves NaN in its row
-        const bool landed = mbar_wait_bounded(smem_addr(&bars[s]), phase);
-        const uint16_t *xr = reinterpret_cast<const uint16_t *>(rows + (size_t)s * stage_bytes);
-        Vec<8> h[NV] = {};
-        float sum = 0.f;
-        float top = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = tid + j * T;
-            if (c < nvec) {
-                h[j] = load_vec<8>(xr + c * 8);
-                if (p.residual)
-                    h[j] = add_vec<8>(h[j], load_vec<8>(xr + p.K + c * 8));
-                if (p.h)
-                    store_vec<8>(p.h + t * p.K + (int64_t)c * 8, h[j]);
-            }
-            count<8, NORM>(h[j], w[j], q8, sum, top);
-        }
-        if (!landed)
-            sum = top = __int_as_float(0x7FFFFFFF);
-        block_reduce(sum, top, s_red[round & 1]);
-        // (every thread has read the row: its stage can take the row `ring` rounds on;
-        // a CTA of one warp has no barrier in its reduction)
-        if (T == 32)
-            __syncwarp();
-        prev = s;
-        if (++s == ring) {
-            s = 0;
-            phase ^= 1u;
-        }
-        if (tid == 0 && t + (int64_t)ring * gridDim.x < M)
-            request(t + (int64_t)ring * gridDim.x, prev);
-        const Factors f = factors<NORM>(p, sum, top);
-        if (q8 && tid == 0)
-            p.s[t] = f.a / kE4m3Max;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = tid + j * T;
-            if (c < nvec)
-                emit<8, NORM>(p, t * p.K + (int64_t)c * 8, h[j], w[j], f);
-        }
-    }
-}
-
 using NormFn = void (*)(NormParams);
-template <int VEC, bool NORM>
+template <int VEC, bool NORM, bool WARP>
 NormFn norm_fn(int nv)
 {
     switch (nv) {
-    case 1: return norm_kernel<VEC, 1, NORM>;
-    case 2: return norm_kernel<VEC, 2, NORM>;
-    case 4: return norm_kernel<VEC, 4, NORM>;
-    default: return norm_kernel<VEC, 0, NORM>;
+    case 1: return norm_kernel<VEC, 1, NORM, WARP>;
+    case 2: return norm_kernel<VEC, 2, NORM, WARP>;
+    case 4: return norm_kernel<VEC, 4, NORM, WARP>;
+    default: return norm_kernel<VEC, 0, NORM, false>;
     }
 }
-
-using NormRowsFn = void (*)(NormParams, int64_t, int);
-template <bool NORM>
-NormRowsFn norm_rows_fn(int nv)
+template <bool NORM, bool WARP>
+NormFn norm_fn_of(int vec, int nv)
 {
-    switch (nv) {
-    case 1: return norm_rows_kernel<1, NORM>;
-    case 2: return norm_rows_kernel<2, NORM>;
-    default: return norm_rows_kernel<4, NORM>;
-    }
-}
-
-// SMs of the current device.
-int sm_count()
-{
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return n;
+    return vec == 8 ? norm_fn<8, NORM, WARP>(nv) : (vec == 2 ? norm_fn<2, NORM, WARP>(nv) : norm_fn<1, NORM, WARP>(nv));
 }
 
 }  // namespace
@@ -434,6 +329,7 @@ cudaError_t launch_norm(const void *x, const void *residual, const void *w, floa
     p.y = static_cast<uint16_t *>(y);
     p.q = static_cast<uint8_t *>(q);
     p.s = s;
+    p.M = M;
     p.K = K;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = st;
@@ -445,41 +341,22 @@ cudaError_t launch_norm(const void *x, const void *residual, const void *w, floa
     // the widest access that every row starts on (the bases are 16-byte aligned)
     const int vec = K % 8 == 0 ? 8 : (K % 2 == 0 ? 2 : 1);
     const int64_t nvec = K / vec;
+    // as few vectors a thread as 256 threads (a warp) hold the row with; a warp a
+    // row from two CTAs of them an SM on (2048 rows of 512 normed with residual to 8
+    // bits: 3.6 us with a CTA a row, 4.4 with a warp; 4096: 5.5 and 5.1)
+    const bool warp = nvec <= 32 * 4 && M >= 2 * 148 * kWarpRows;
     int nv = 1;
-    while (nv < 4 && nvec > (int64_t)256 * nv)
+    while (nv < 4 && nvec > (int64_t)(warp ? 32 : 256) * nv)
         nv *= 2;
-    int64_t threads = (nvec + nv - 1) / nv;
-    threads = (threads + 31) / 32 * 32;
-    // many rows: the pipelined kernel, when an SM's shared memory holds at least
-    // two rows of two CTAs (or three of one) and each CTA has several rows
-    const int sms = vec == 8 && threads <= 512 && M >= 4 * 148 ? sm_count() : 0;
-    if (sms > 0) {
-        const size_t stage = (size_t)K * 2 * (residual ? 2 : 1);
-        const size_t room = 220 * 1024;
-        int per_sm = (int)std::min<int64_t>(16, rows_per_sm(nv, w != nullptr) * (nv == 4 ? 512 : 256) / threads);
-        while (per_sm > 1 && room / per_sm < 2 * stage + 1024)
-            --per_sm;
-        const int ring = (int)std::min<size_t>(kRing, (room / per_sm - 1024) / stage);
-        if (ring >= (per_sm > 1 ? 2 : 3)) {
-            const NormRowsFn fn = w ? norm_rows_fn<true>(nv) : norm_rows_fn<false>(nv);
-            const size_t smem = ring * stage;
-            const cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(fn), smem);
-            if (e != cudaSuccess)
-                return e;
-            cfg.gridDim = dim3((unsigned)std::min<int64_t>(M, (int64_t)per_sm * sms));
-            cfg.blockDim = dim3((unsigned)threads);
-            cfg.dynamicSmemBytes = smem;
-            return cudaLaunchKernelEx(&cfg, fn, p, M, ring);
-        }
-    }
+    int64_t threads = warp ? 32 * kWarpRows : ((nvec + nv - 1) / nv + 31) / 32 * 32;
     if (threads > 1024) {
         threads = 1024;
         nv = 0;
     }
-    cfg.gridDim = dim3((unsigned)M);
+    cfg.gridDim = dim3((unsigned)(warp ? (M + kWarpRows - 1) / kWarpRows : M));
     cfg.blockDim = dim3((unsigned)threads);
-    const NormFn fn = w ? (vec == 8 ? norm_fn<8, true>(nv) : (vec == 2 ? norm_fn<2, true>(nv) : norm_fn<1, true>(nv)))
-                        : (vec == 8 ? norm_fn<8, false>(nv) : (vec == 2 ? norm_fn<2, false>(nv) : norm_fn<1, false>(nv)));
+    const NormFn fn = w ? (warp ? norm_fn_of<true, true>(vec, nv) : norm_fn_of<true, false>(vec, nv))
+                        : (warp ? norm_fn_of<false, true>(vec, nv) : norm_fn_of<false, false>(vec, nv));
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
