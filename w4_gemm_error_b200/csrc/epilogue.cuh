@@ -25,9 +25,15 @@ struct Epilogue {
     const float *xs = nullptr;            // [M] scale of each token's e4m3 activations (kQ8)
 };
 
-// 1 / (1 + exp(-c)), by the hardware's exp2 and reciprocal.  They are off by a
-// few units of 2^-23 |c| at most, far inside the bf16 rounding of the result; a
-// large negative c gives exp = inf and a sigmoid of zero.
+// v / (1 + exp(-c)), by the hardware's exp2 and reciprocal:  with t = 2^-7 exp(-c / 2),
+//   (2^-14 v) / (2^-14 + t^2).
+// Both instructions flush what leaves the normal numbers, and exp(-c) itself does
+// so from |c| = 88 on, where the result still is a bf16 value; t and the
+// denominator do so from c = -97 on, where the result is below bf16's smallest
+// value (2^-133).  The exponent of t, |c| log2(e) / 2 + 7, is off by a unit in its
+// last place at most, so the result by a few units of 2^-23 max(8, |c|), far inside
+// its bf16 rounding; 2^-14 v is inexact below |v| = 2^-112 and moves the result by
+// less than 2^-135 there.  A large negative c gives t = inf and a zero.
 __device__ __forceinline__ float ex2_approx(float x)
 {
     float y;
@@ -40,11 +46,13 @@ __device__ __forceinline__ float rcp_approx(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kHalfLog2e = 0.7213475204444817f;
+constexpr float kSig = 0x1p-14f;
 constexpr float kGeluK = 1.5957691216057308f, kGeluK3 = 0.071354816272600f;   // 2 sqrt(2/pi), and times 0.044715
 __device__ __forceinline__ float times_sigmoid(float v, float c)
 {
-    return v * rcp_approx(1.0f + ex2_approx(-kLog2e * c));
+    const float t = ex2_approx(fmaf(-kHalfLog2e, c, -7.0f));
+    return kSig * v * rcp_approx(fmaf(t, t, kSig));
 }
 
 __device__ __forceinline__ float activate(float v, int act)
@@ -106,9 +114,10 @@ __device__ __forceinline__ f32x2 activate2(f32x2 v)
         if constexpr (ACT == kActGeluTanh)
             c = f2_mul(v, f2_fma(f2_pack(kGeluK3, kGeluK3), f2_mul(v, v), f2_pack(kGeluK, kGeluK)));
         float a, b;
-        f2_unpack(f2_mul(c, f2_pack(-kLog2e, -kLog2e)), a, b);
-        f2_unpack(f2_add(f2_pack(ex2_approx(a), ex2_approx(b)), f2_pack(1.f, 1.f)), a, b);
-        return f2_mul(v, f2_pack(rcp_approx(a), rcp_approx(b)));
+        f2_unpack(f2_fma(c, f2_pack(-kHalfLog2e, -kHalfLog2e), f2_pack(-7.f, -7.f)), a, b);
+        const f32x2 t = f2_pack(ex2_approx(a), ex2_approx(b));
+        f2_unpack(f2_fma(t, t, f2_pack(kSig, kSig)), a, b);
+        return f2_mul(f2_mul(v, f2_pack(kSig, kSig)), f2_pack(rcp_approx(a), rcp_approx(b)));
     } else {
         float a, b;
         f2_unpack(v, a, b);
