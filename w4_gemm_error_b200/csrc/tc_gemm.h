@@ -36,7 +36,7 @@ cudaError_t launch_tc(const Packed &pk, const void *x, void *y, int64_t M, const
 
 // ---- the forms kEpi and kQ8 of epilogue.cuh
 
-// Two constants a token of form kQ8, 2^9 xs[t] and 2^-9 sum_k xq[t,k], pairs of
+// Two constants a token of form kQ8, xs[t] and 2^-9 sum_k xq[t,k], pairs of
 // tokens together (c0[2i], c0[2i+1], c1[2i], c1[2i+1]); whole chunks of 32
 // tokens are allocated.  Index of c0; c1 is 2 on.
 __host__ __device__ constexpr int64_t rowc_at(int64_t t) { return 4 * (t / 2) + (t & 1); }

@@ -123,7 +123,8 @@ __device__ __forceinline__ void emit_chunk(uint32_t tacc, float e_n, float z_n, 
             f32x2 k = e2;
             if constexpr (FORM == kQ8) {
                 k = f2_mul(e2, f2_pack(c[j / 2].x, c[j / 2].y));
-                v = f2_fma(nz2, f2_pack(c[j / 2].z, c[j / 2].w), v);
+                // (2^9 beside the sum: with a scale of 2^119 or more it would leave fp32)
+                v = f2_mul(f2_fma(nz2, f2_pack(c[j / 2].z, c[j / 2].w), v), f2_pack(512.f, 512.f));
             }
             v = activate2<ACT>(f2_fma(k, v, bias2));
             if (MUL)

@@ -5,7 +5,7 @@
 //   D[t, j] = x[t,:] . G[j,:],  G = [w_g; A^T] (R1p rows)
 //   kEpi: v = g D[t,1+j],         g = 1 / (1 + exp(-(D[t,0] + b_g)))
 //   kQ8:  v = 2^-9 g D[t,1+j],    g = 1 / (1 + exp(-(xs[t] D[t,0] + b_g))),
-//         rowc: 2^9 xs[t] and 2^-9 X_t,  X_t = sum_k xq[t,k]
+//         rowc: xs[t] and 2^-9 X_t,  X_t = sum_k xq[t,k]
 //   (v rounded to tf32)
 //
 // A cluster of S CTAs takes 128 tokens; CTA q the 64-k blocks q, q + S, ...
@@ -297,7 +297,7 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         float xs = 1.f;
         if constexpr (FORM == kQ8) {
             xs = __ldg(p.xs + t);
-            p.rowc[rowc_at(t)] = 512.0f * xs;
+            p.rowc[rowc_at(t)] = xs;
             p.rowc[rowc_at(t) + 2] = sums[tid * ld + p.R1p] * (1.0f / 512.0f);
         }
         if (ec)

@@ -81,7 +81,7 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     __shared__ __align__(8) uint64_t bars[2 * STAGES + 2];   // ready and empty of each stage; done; drain
     __shared__ uint32_t tmem_base_slot;
     __shared__ volatile int abort_flag;
-    __shared__ float2 s_const[FORM == kQ8 ? BN : 1];   // 2^9 xs[t], 2^-9 sum_k xq[t,k] of this CTA's outputs
+    __shared__ float2 s_const[FORM == kQ8 ? BN : 1];   // xs[t], 2^-9 sum_k xq[t,k] of this CTA's outputs
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -298,7 +298,7 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             float x = 0.f;
             for (int s = 0; s < S; ++s)
                 x += ld_dsmem_f32(map_to_rank(base + (uint32_t)(BN * BM + first + tid) * 4, (uint32_t)s));
-            s_const[tid] = make_float2(512.0f * __ldg(p.epi.xs + t0 + first + tid), x * (1.0f / 512.0f));
+            s_const[tid] = make_float2(__ldg(p.epi.xs + t0 + first + tid), x * (1.0f / 512.0f));
         }
         __syncthreads();
     }
@@ -335,8 +335,9 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             }
             if constexpr (FORM == kQ8) {
                 const float2 c = s_const[tt];
-                v0 = e0 * c.x * (v0 - z0 * c.y);
-                v1 = e1 * c.x * (v1 - z1 * c.y);
+                // (2^9 beside the sum: with a scale of 2^119 or more it would leave fp32)
+                v0 = e0 * c.x * (512.0f * (v0 - z0 * c.y));
+                v1 = e1 * c.x * (512.0f * (v1 - z1 * c.y));
             } else {
                 v0 *= e0;
                 v1 *= e1;
