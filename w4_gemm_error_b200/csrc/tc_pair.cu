@@ -70,6 +70,11 @@ constexpr int HALF_SLOT = CHUNK * BM * 2;   // residual / y; a second one for th
 constexpr int ROWC_BYTES = CHUNK * 8;
 constexpr int EPI_WARP = 4, DEQ_WARP = 12, GROUP_WARPS = 4, GROUPS = 4;
 constexpr int THREADS = 32 * (DEQ_WARP + GROUPS * GROUP_WARPS);
+// What a CTA adds to an accumulator's hand-back: its epilogue warps and the prefetching
+// warp, each when it has seen the accumulator full.  Whoever waits for a phase of
+// `tfull` has to be counted, or that phase and the next could pass unseen, and the
+// one after them, of the same parity, may never come.
+constexpr int HAND_BACK = DEQ_WARP - EPI_WARP + 1;
 
 // Ring depth and shared memory with and without a multiplier in the slots.
 int pair_stages(bool mul) { return mul ? 5 : 6; }
@@ -178,7 +183,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     const uint32_t ready0 = smem_addr(&bars[0]);
     const uint32_t empty0 = smem_addr(&bars[MAX_STAGES]);
     const uint32_t tfull0 = smem_addr(&bars[2 * MAX_STAGES]);
-    const uint32_t tempty0 = smem_addr(&bars[2 * MAX_STAGES + 2]);   // first CTA's: both epilogues are done
+    const uint32_t tempty0 = smem_addr(&bars[2 * MAX_STAGES + 2]);   // first CTA's: HAND_BACK arrivals of each CTA
     const uint32_t sfull0 = smem_addr(&bars[2 * MAX_STAGES + 4]);
     const uint32_t sempty0 = smem_addr(&bars[2 * MAX_STAGES + 4 + NSLOT]);
     const uint32_t drain = smem_addr(&bars[2 * MAX_STAGES + 4 + 2 * NSLOT]);
@@ -196,7 +201,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, 2 * 8);
+            mbar_init(tempty0 + 8 * b, 2 * HAND_BACK);
         }
         for (int s = 0; s < NSLOT; ++s) {
             mbar_init(sfull0 + 8 * s, 1);
@@ -406,6 +411,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
                 prefetch(u + n_clusters);
                 if (!mbar_wait(tfull0 + 8 * (lt & 1), (lt >> 1) & 1, &abort_flag, p.status))
                     break;
+                mbar_arrive_remote(tempty0 + 8 * (lt & 1), 0);
             }
         }
     } else if (warp >= EPI_WARP && warp < DEQ_WARP) {
