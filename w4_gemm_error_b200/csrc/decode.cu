@@ -617,7 +617,7 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             if (mine && n < p.N)
                 eo[i] = epi_load(p.epi, t, n, p.N);
             if constexpr (FORM == kQ8)
-                xs_epi[i] = mine ? __ldg(p.epi.xs + t) : 0.f;
+                xs_epi[i] = mine ? p.epi.xs[t] : 0.f;
         }
     }
 

@@ -108,19 +108,19 @@ __host__ __device__ constexpr uint32_t rows_tail_bytes(int W, int rp)
 // Eight consecutive activations as the pairs that enter the MMA.  e4m3 (form
 // kQ8) becomes f16 for the row CTAs, whose weights are small integers, and
 // bf16 for the CTAs of u, whose G rows are bf16; both conversions are exact,
-// so the products are those of the 8-bit values themselves.
+// so the products are those of the 8-bit values themselves.  x: settled.
 template <int FORM>
 __device__ __forceinline__ uint4 load_x8(const void *x, int64_t i, bool is_u)
 {
     if constexpr (FORM == kQ8) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(x) + i));
+        const uint2 q = ld_settled8(static_cast<const uint8_t *>(x) + i);
         uint4 v = make_uint4(e4m3x2_to_f16x2((uint16_t)q.x), e4m3x2_to_f16x2((uint16_t)(q.x >> 16)),
                              e4m3x2_to_f16x2((uint16_t)q.y), e4m3x2_to_f16x2((uint16_t)(q.y >> 16)));
         if (is_u)
             v = make_uint4(f16x2_to_bf16x2(v.x), f16x2_to_bf16x2(v.y), f16x2_to_bf16x2(v.z), f16x2_to_bf16x2(v.w));
         return v;
     } else {
-        return ld_nc(static_cast<const uint16_t *>(x) + i);
+        return ld_settled(static_cast<const uint16_t *>(x) + i);
     }
 }
 
@@ -254,6 +254,7 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
         };
         const int sb0 = warp * nsb_cta / W, sb1 = (warp + 1) * nsb_cta / W;
         pdl_wait();
+        const void *const x = settled(static_cast<const uint8_t *>(p.x));
         // epilogue operands of this thread's output, in flight during the product
         EpiOperands eo;
         float xs_epi = 1.f;
@@ -263,7 +264,7 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             if (!is_u && tid < kEpi && t < p.M && n < p.N) {
                 eo = epi_load(p.epi, t, n, p.N);
                 if (FORM == kQ8)
-                    xs_epi = __ldg(p.epi.xs + t);
+                    xs_epi = p.epi.xs[t];
             }
         }
         bool ok = true;
@@ -279,7 +280,7 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             for (int c = tid; c < mrows * per_row; c += kConsumers) {
                 const int t = c / per_row, c8 = c - t * per_row;
                 const int64_t k = kbase + 8 * c8;
-                const uint4 v = k < p.K ? load_x8<FORM>(p.x, (int64_t)t * p.K + k, false) : make_uint4(0, 0, 0, 0);
+                const uint4 v = k < p.K ? load_x8<FORM>(x, (int64_t)t * p.K + k, false) : make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4 *>(xs + t * xst + 8 * c8) = v;
             }
             named_bar_sync(2, kConsumers);
@@ -313,8 +314,8 @@ decode_rows_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 for (int n = 0; n < T; ++n) {
                     const int64_t t = 8 * n + gid;
                     if (t < p.M && k < p.K) {
-                        dst[n][0] = load_x8<FORM>(p.x, t * p.K + k, is_u);
-                        dst[n][1] = load_x8<FORM>(p.x, t * p.K + k + 8, is_u);
+                        dst[n][0] = load_x8<FORM>(x, t * p.K + k, is_u);
+                        dst[n][1] = load_x8<FORM>(x, t * p.K + k + 8, is_u);
                     } else {
                         dst[n][0] = make_uint4(0, 0, 0, 0);
                         dst[n][1] = dst[n][0];

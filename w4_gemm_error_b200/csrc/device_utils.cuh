@@ -130,6 +130,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
 }
 
+// Loads through the read-only path (ld_stream, ld_nc and __ldg): for the layer's own
+// weights alone.  The path is for memory that nothing writes while the kernel
+// runs, and a kernel launched with programmatic serialization runs beside the
+// earlier ones that write its operands; the compiler may also move such a load
+// above the wait for them.  Operands take plain loads, or ld_settled.
+
 // Streaming 16-byte load that is read once (no L1 allocation).
 __device__ __forceinline__ uint4 ld_stream(const void *p)
 {
@@ -154,6 +160,28 @@ __device__ __forceinline__ void pdl_launch_dependents()
 __device__ __forceinline__ void pdl_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// An operand's address after pdl_wait(): loads through it come after the wait,
+// and may otherwise be moved freely by the compiler (a plain load may not pass
+// the stores before it).
+template <class T>
+__device__ __forceinline__ const T *settled(const T *p)
+{
+    asm volatile("" : "+l"(p)::"memory");
+    return p;
+}
+__device__ __forceinline__ uint4 ld_settled(const void *p)
+{
+    uint4 v;
+    asm("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_settled8(const void *p)
+{
+    uint2 v;
+    asm("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
 }
 
 // fp32 rounded to the tf32 grid (10 explicit mantissa bits, round to nearest, ties away).

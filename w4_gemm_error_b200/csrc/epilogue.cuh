@@ -126,8 +126,8 @@ __device__ __forceinline__ f32x2 activate2(f32x2 v)
 }
 
 // The operands of output (t, n): loaded apart from their use, so that the
-// loads are in flight while the product is formed.  mul and residual are read
-// with plain loads, since either may be the memory of y.
+// loads are in flight while the product is formed.  Plain loads: an earlier kernel
+// that still runs may write them, and mul and residual may be the memory of y.
 struct EpiOperands {
     float bias = 0.f, mul = 1.f, residual = 0.f;
 };
@@ -136,7 +136,7 @@ __device__ __forceinline__ EpiOperands epi_load(const Epilogue &e, int64_t t, in
 {
     EpiOperands o;
     if (e.bias)
-        o.bias = bf16_lo(__ldg(e.bias + n));
+        o.bias = bf16_lo(e.bias[n]);
     if (e.mul)
         o.mul = bf16_lo(e.mul[t * N + n]);
     if (e.residual)

@@ -62,6 +62,7 @@ template <int MT, int MINB, bool PUSH>
 __global__ void __launch_bounds__(128, MINB) prepass_kernel(PrepassParams p)
 {
     pdl_wait();  // x is written by the previous kernel in the stream
+    const uint16_t *const x = settled(p.x);
     // the next kernel may start now: x is complete (a tcgen05 kernel that starts
     // early reads it without waiting)
     pdl_launch_dependents();
@@ -92,10 +93,10 @@ __global__ void __launch_bounds__(128, MINB) prepass_kernel(PrepassParams p)
             const int64_t t = t0 + 8 * n + gid;
             uint4 a = make_uint4(0, 0, 0, 0), b = a;
             if (t < p.M && k < p.K) {
-                const uint16_t *src = p.x + t * p.K + k;
-                a = ld_nc(src);
+                const uint16_t *src = x + t * p.K + k;
+                a = ld_settled(src);
                 if (k + 8 < p.K)
-                    b = ld_nc(src + 8);
+                    b = ld_settled(src + 8);
             }
             xb[n][0] = a.x; xb[n][1] = a.y; xb[n][2] = a.z; xb[n][3] = a.w;
             xb[n][4] = b.x; xb[n][5] = b.y; xb[n][6] = b.z; xb[n][7] = b.w;

@@ -435,7 +435,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             const float sn = n < p.N ? p.s[n] : 0.f;
             const float e_n = sn != 0.0f ? sn : 1.0f;   // the EC operand was divided by it
             const float z_n = FORM == kQ8 && sn != 0.0f ? (float)p.z[n] : 0.f;
-            const float bias = p.epi.bias && n < p.N ? bf16_lo(__ldg(p.epi.bias + n)) : 0.f;
+            const float bias = p.epi.bias && n < p.N ? bf16_lo(p.epi.bias[n]) : 0.f;
             ok = ok && mbar_wait(tfull0 + 8 * buf, (lt >> 1) & 1, &abort_flag, p.status);
             tc_fence_after();
             for (int c = 0; n0 < p.N && c < BN / CHUNK && t0 + c * CHUNK < p.M; ++c, ++g) {

@@ -296,7 +296,7 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const int64_t t = t0 + first + tid;
         float xs = 1.f;
         if constexpr (FORM == kQ8) {
-            xs = __ldg(p.xs + t);
+            xs = p.xs[t];
             p.rowc[rowc_at(t)] = xs;
             p.rowc[rowc_at(t) + 2] = sums[tid * ld + p.R1p] * (1.0f / 512.0f);
         }

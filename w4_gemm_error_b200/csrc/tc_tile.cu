@@ -298,7 +298,7 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             float x = 0.f;
             for (int s = 0; s < S; ++s)
                 x += ld_dsmem_f32(map_to_rank(base + (uint32_t)(BN * BM + first + tid) * 4, (uint32_t)s));
-            s_const[tid] = make_float2(__ldg(p.epi.xs + t0 + first + tid), x * (1.0f / 512.0f));
+            s_const[tid] = make_float2(p.epi.xs[t0 + first + tid], x * (1.0f / 512.0f));
         }
         __syncthreads();
     }
@@ -316,7 +316,7 @@ tc_tile_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             z0 = sn.x != 0.f ? (float)(z & 255u) : 0.f;
             z1 = sn.y != 0.f ? (float)(z >> 8) : 0.f;
         }
-        const uint32_t bias = p.epi.bias ? __ldg(reinterpret_cast<const uint32_t *>(p.epi.bias + n)) : 0u;
+        const uint32_t bias = p.epi.bias ? *reinterpret_cast<const uint32_t *>(p.epi.bias + n) : 0u;
 #pragma unroll 1
         for (int tt = tid / (BM / 2); tt < ntok; tt += THREADS / (BM / 2)) {
             const int64_t at = (int64_t)(t0 + first + tt) * p.N + n;
