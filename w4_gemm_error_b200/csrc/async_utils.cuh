@@ -38,6 +38,12 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
+// Arrive, with the release semantics that an arrival has by default: every earlier
+// load and store of this thread, and of the threads that it has met in a barrier
+// since (__syncwarp), is performed before a waiter sees the phase complete.  So a
+// lane that arrives after __syncwarp releases what its whole warp has read, and
+// the copy that the waiter then issues cannot overwrite it too early; that the
+// values' arithmetic may come later does not matter, since they are in registers.
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -134,16 +140,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             return false;
         }
     }
-}
-
-// Before a warp arrives on a barrier that lets the next copy overwrite what it
-// has read: `seen` is made from every lane's loads.  The arithmetic on the
-// loaded values may be scheduled after the arrival, so that nothing else waits
-// for them; a branch on them does (without it, sums came out wrong).
-__device__ __forceinline__ void loads_complete(uint32_t seen)
-{
-    if (__all_sync(0xffffffffu, seen == 0x9E3779B9u))
-        __nanosleep(0);
 }
 
 // A warp's wait: every lane waits, all learn the same outcome.

@@ -390,7 +390,6 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             if (!ok)
                 break;
             const uint8_t *ctile = bp + L.ring + s * kStage;
-            uint32_t seen = 0u;
 #pragma unroll
             for (int i = 0; i < 4 / KPAR; ++i) {
                 const int sb = KPAR * i + kq;
@@ -401,11 +400,8 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 const uint8_t *xt = ctile + 8192 + sb * kXTile;
                 uint4 xv[T][2];
 #pragma unroll
-                for (int n = 0; n < T; ++n) {
+                for (int n = 0; n < T; ++n)
                     read_x16<FORM>(xt, 8 * n + gid, cl, false, xv[n]);
-                    seen ^= xv[n][0].x ^ xv[n][1].x;
-                }
-                seen ^= wgv.x ^ whv.x;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t wgw = j ? wgv.y : wgv.x, whw = j ? whv.y : whv.x;
@@ -425,8 +421,6 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 }
             }
             // every lane's shared-memory reads of this stage are done: release it
-            if constexpr (FORM == kQ8)
-                loads_complete(seen);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_empty + 8 * s);
@@ -458,7 +452,6 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
             if (!ok)
                 break;
             const uint8_t *stage = bp + L.ring + s * kStage;
-            uint32_t seen = 0u;
             for (int j = 0; j < 4; ++j) {
                 if ((4 * c + j) % W != warp)
                     continue;
@@ -469,14 +462,12 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                 const uint4 a1 = *reinterpret_cast<const uint4 *>(gt + ra * 128 + (((2 * cl + 1) ^ (ra & 7)) << 4));
                 const uint4 b0 = *reinterpret_cast<const uint4 *>(gt + rb * 128 + (((2 * cl) ^ (rb & 7)) << 4));
                 const uint4 b1 = *reinterpret_cast<const uint4 *>(gt + rb * 128 + (((2 * cl + 1) ^ (rb & 7)) << 4));
-                seen ^= a0.x ^ a1.x ^ b0.x ^ b1.x;
                 const uint32_t ga[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
                 const uint32_t ha[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
                 for (int n = 0; n < T; ++n) {
                     uint4 xv[2];
                     read_x16<FORM>(xt, 8 * n + gid, cl, true, xv);
-                    seen ^= xv[0].x ^ xv[1].x;
                     const uint32_t xa[8] = {xv[0].x, xv[0].y, xv[0].z, xv[0].w,
                                             xv[1].x, xv[1].y, xv[1].z, xv[1].w};
                     // natural pairs: step s covers k = 16 cl + 4s + {0,1} and + {2,3}
@@ -486,8 +477,6 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                                        ha[2 * q + 1], xa[2 * q], xa[2 * q + 1]);
                 }
             }
-            if constexpr (FORM == kQ8)
-                loads_complete(seen);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_empty + 8 * s);
