@@ -18,6 +18,8 @@
 // All sums are fp32; v is rounded once to each output type.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "async_utils.cuh"
 #include "handle.h"
 #include "norm.h"
@@ -296,6 +298,23 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_kernel(Norm
     }
 }
 
+// SMs of the current device (asked for once a device).
+int sm_count()
+{
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev < kMaxDevices)
+        n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+            return 1;   // (the launch will report what is wrong)
+        if (dev < kMaxDevices)
+            known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 using NormFn = void (*)(NormParams);
 template <int VEC, bool NORM, bool WARP>
 NormFn norm_fn(int nv)
@@ -346,8 +365,9 @@ cudaError_t launch_norm(const void *x, const void *residual, const void *w, floa
     // 95 us instead of 85: fewer CTAs an SM to fill each other's waits); a warp a
     // row from two CTAs of them an SM on (2048 rows of 512 normed with residual to 8
     // bits: 3.6 us with a CTA a row, 4.4 with a warp; 4096: 5.5 and 5.1)
-    const bool warp = nvec <= 32 * 4 && M >= 2 * 148 * kWarpRows;
-    const int span = warp ? 32 : (M <= 148 ? 512 : 256);
+    const int64_t sms = sm_count();
+    const bool warp = nvec <= 32 * 4 && M >= 2 * sms * kWarpRows;
+    const int span = warp ? 32 : (M <= sms ? 512 : 256);
     int nv = 1;
     while (nv < 4 && nvec > (int64_t)span * nv)
         nv *= 2;
