@@ -394,7 +394,11 @@ def _cuda_rows(x, name):
     return M, K, index
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# torch's own functions behind current_stream() and current_device(), where it has them (a
+# torch built without CUDA does not; these cost a tenth of a microsecond instead of one)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream_on(stream, index) -> int:
@@ -406,7 +410,7 @@ def _stream_on(stream, index) -> int:
 
 def _call_on(index, f, call, *args):
     """f(*args) with device `index` current (for calls that run on the current device)."""
-    if torch._C._cuda_getDevice() == index:
+    if _current_device() == index:
         rc = f(*args)
     else:
         with torch.cuda.device(index):
