@@ -273,19 +273,16 @@ tc_prepass2_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         float *const own = part + kTok * ld;
         for (int i = tid; i < mine * nv; i += kThreads) {
             const uint32_t a = base + (uint32_t)(first * ld + 4 * i) * 4;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int s0 = 0; s0 < S; s0 += 8) {   // (eight loads in flight; S is a power of two)
-                float4 v[8];
+            float4 v[kMaxCluster], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    v[s] = s0 + s < S ? ld_dsmem_f4(map_to_rank(a, (uint32_t)(s0 + s))) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s = 0; s < kMaxCluster; ++s)   // (all loads in flight)
+                v[s] = s < S ? ld_dsmem_f4(map_to_rank(a, (uint32_t)s)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    sum.x += v[s].x;
-                    sum.y += v[s].y;
-                    sum.z += v[s].z;
-                    sum.w += v[s].w;
-                }
+            for (int s = 0; s < kMaxCluster; ++s) {
+                sum.x += v[s].x;
+                sum.y += v[s].y;
+                sum.z += v[s].z;
+                sum.w += v[s].w;
             }
             reinterpret_cast<float4 *>(own)[i] = sum;
         }
