@@ -374,10 +374,21 @@ def _dev(t, dtype, shape, name, index):
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
 
 
-def _out(t, dtype, shape, name, x):
+def _new(shape, dtype, device, stream):
+    """A new output of a call on ``stream``, in that stream's memory: a block of the current
+    stream's may still be in use there by earlier work, which the call does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(t, dtype, shape, name, x, stream):
     """(tensor, address) of an output: the caller's, checked, or a new one beside x."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=x.device)
+        t = _new(shape, dtype, x.device, stream)
         return t, t.data_ptr()
     return t, _dev(t, dtype, shape, name, x.get_device())
 
@@ -441,12 +452,12 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
     y = q = s = h = py = pq = ps = ph = pr = None
     if residual is not None:
         pr = _dev(residual, tb, rows, "residual", dev)
-        h, ph = _out(out_sum, tb, rows, "out_sum", x)
+        h, ph = _out(out_sum, tb, rows, "out_sum", x, stream)
     if bf16:
-        y, py = _out(out, tb, rows, "out", x)
+        y, py = _out(out, tb, rows, "out", x, stream)
     if q8:
-        q, pq = _out(out_q, torch.float8_e4m3fn, rows, "out_q", x)
-        s, ps = _out(out_s, torch.float32, (M,), "out_s", x)
+        q, pq = _out(out_q, torch.float8_e4m3fn, rows, "out_q", x, stream)
+        s, ps = _out(out_s, torch.float32, (M,), "out_s", x, stream)
     _call_on(dev, _lib.spear_w4ec_rmsnorm, "spear_w4ec_rmsnorm", px, pr, pw, eps, M, K, ph, py, pq, ps,
              _stream_on(stream, dev))
     return y, q, s, h
@@ -459,8 +470,8 @@ def quantize_q8(x: torch.Tensor, *, out_q: torch.Tensor | None = None, out_s: to
     M, K, dev = _cuda_rows(x, "x")
     rows = (M, K)
     px = _dev(x, torch.bfloat16, rows, "x", dev)
-    q, pq = _out(out_q, torch.float8_e4m3fn, rows, "out_q", x)
-    s, ps = _out(out_s, torch.float32, (M,), "out_s", x)
+    q, pq = _out(out_q, torch.float8_e4m3fn, rows, "out_q", x, stream)
+    s, ps = _out(out_s, torch.float32, (M,), "out_s", x, stream)
     _call_on(dev, _lib.spear_w4ec_quantize_q8, "spear_w4ec_quantize_q8", px, M, K, pq, ps, _stream_on(stream, dev))
     return q, s
 
@@ -514,7 +525,7 @@ class W4ECLinear:
     def forward(self, x: torch.Tensor, flags: int = 0, out: torch.Tensor | None = None, stream=None):
         M = x.shape[0]
         _dev_bf16(x, (M, self.K), "x")
-        y = out if out is not None else torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
+        y = out if out is not None else _new((M, self.N), torch.bfloat16, x.device, stream)
         _dev_bf16(y, (M, self.N), "y")
         spear_w4ec_forward(self.h, x, y, M, flags, stream)
         return y
@@ -545,7 +556,7 @@ class W4ECLinear:
         and residual bf16 [M, N] (each may be ``out`` itself)."""
         M, _, dev = _cuda_rows(x, "x")
         px = _dev(x, torch.bfloat16, (M, self.K), "x", dev)
-        y, py = _out(out, torch.bfloat16, (M, self.N), "out", x)
+        y, py = _out(out, torch.bfloat16, (M, self.N), "out", x, stream)
         ep = self._epilogue(M, act, bias, mul, residual, dev)
         rc = _lib.spear_w4ec_forward_ep(self.h, px, py, M, ep, flags, _stream_on(stream, dev))
         if rc:
@@ -560,7 +571,7 @@ class W4ECLinear:
         M, _, dev = _cuda_rows(xq, "xq")
         px = _dev(xq, torch.float8_e4m3fn, (M, self.K), "xq", dev)
         ps = _dev(xs, torch.float32, (M,), "xs", dev)
-        y, py = _out(out, torch.bfloat16, (M, self.N), "out", xq)
+        y, py = _out(out, torch.bfloat16, (M, self.N), "out", xq, stream)
         ep = self._epilogue(M, act, bias, mul, residual, dev)
         rc = _lib.spear_w4ec_forward_q8(self.h, px, ps, py, M, ep, flags, _stream_on(stream, dev))
         if rc:
@@ -568,16 +579,16 @@ class W4ECLinear:
         return y
 
     def packed(self, stream=None):
-        codes = torch.empty((self.N, self.K // 8), dtype=torch.int32, device=self.device)
-        s = torch.empty(self.N, dtype=torch.float32, device=self.device)
-        z = torch.empty(self.N, dtype=torch.uint8, device=self.device)
+        codes = _new((self.N, self.K // 8), torch.int32, self.device, stream)
+        s = _new((self.N,), torch.float32, self.device, stream)
+        z = _new((self.N,), torch.uint8, self.device, stream)
         spear_w4ec_get_packed(self.h, codes, s, z, stream)
         return codes, s, z
 
     def gate(self, x: torch.Tensor, stream=None):
         M = x.shape[0]
         _dev_bf16(x, (M, self.K), "x")
-        g = torch.empty(M, dtype=torch.float32, device=x.device)
+        g = _new((M,), torch.float32, x.device, stream)
         spear_w4ec_get_gate(self.h, x, g, M, stream)
         return g
 
@@ -663,7 +674,7 @@ class W4ECStack:
     def forward(self, x: torch.Tensor, flags: int = 0, out: torch.Tensor | None = None, stream=None):
         M = x.shape[0]
         _dev_bf16(x, (M, self.in_width), "x")
-        y = out if out is not None else torch.empty((M, self.out_width), dtype=torch.bfloat16, device=x.device)
+        y = out if out is not None else _new((M, self.out_width), torch.bfloat16, x.device, stream)
         _dev_bf16(y, (M, self.out_width), "y")
         spear_w4ec_stack_forward(self.h, x, y, M, flags, stream)
         return y
@@ -800,7 +811,7 @@ class W4ECRowParallel:
         spear_w4ec_tp_partial(self.h, x, M, flags, stream)
 
     def reduce(self, M: int, flags: int = 0, out: torch.Tensor | None = None, stream=None):
-        y = out if out is not None else torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
+        y = out if out is not None else _new((M, self.N), torch.bfloat16, self.device, stream)
         _dev_bf16(y, (M, self.N), "y")
         spear_w4ec_tp_reduce(self.h, y, M, flags, stream)
         return y
@@ -808,7 +819,7 @@ class W4ECRowParallel:
     def forward(self, x: torch.Tensor, flags: int = 0, out: torch.Tensor | None = None, stream=None):
         M = x.shape[0]
         _dev_bf16(x, (M, self.K), "x")
-        y = out if out is not None else torch.empty((M, self.N), dtype=torch.bfloat16, device=x.device)
+        y = out if out is not None else _new((M, self.N), torch.bfloat16, x.device, stream)
         _dev_bf16(y, (M, self.N), "y")
         spear_w4ec_tp_forward(self.h, x, y, M, flags, stream)
         return y
