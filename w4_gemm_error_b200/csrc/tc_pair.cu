@@ -582,15 +582,26 @@ using PairFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUte
 //   8192 x 512, r 64    1024 tokens (K in 2)  31.2 / 24.9 against 49.3 / 32.2
 //                       1536 tokens (whole)   52.4 / 40.2 against 51.1 / 33.1
 //   2048 x 512, no EC   4096 tokens (whole)   21.6 / 17.5 against 18.5 / 22.2
-// The last one, in 8 bits, needs a prepass (of the code sums) for the pairs alone:
-// there they are taken from more tiles than SMs on.
+// In 8 bits without the EC the pairs alone need a prepass (of the code sums).  It
+// reads all the tokens, so its cost grows with them, and what the pairs win with the
+// channels: there they are taken, while the tiles have an SM each, up to as many
+// blocks of 128 tokens as of 128 channels.  Tile against pair:
+//   14336 x 4096   256 tokens (K in 2) 33.6 against 52.3, 320 55.9 / 53.1, 512 58.3 / 54.2, 640 110.2 / 55.5
+//    4096 x 4096   256 tokens (K in 2) 17.1 against 22.4, 320 24.1 / 22.6, 512 25.6 / 23.2
+//     512 x 4096   384 tokens 13.3 against 12.6, 512 13.7 / 12.6
+//    4096 x 14336   40 tokens 18.8 against 19.7, 64 20.2 / 19.8, 128 25.1 / 21.0
+//     512 x 14336  128 tokens 13.5 against 10.2
+//    1032 x 2744   400 tokens 16.7 against 16.8, 513 17.2 / 17.6, 700 19.2 / 18.4
+//   28672 x 1024  1300 tokens 100.9 against 95.5, 2000 101.6 / 117.0
+//    8192 x 512   4096 tokens 39.2 against 44.4
+//    2048 x 512   4096 tokens 18.9 against 21.8, 5000 (more tiles than SMs) 35.1 / 23.4
 bool tc_use_pair(const Packed &pk, int64_t M, bool ec, int form, int num_sms)
 {
     if (M <= (form == kQ8 ? 32 : 64))
         return false;
     const int64_t tok = M <= 64 ? 64 : 128, tiles = (M + tok - 1) / tok * (pk.Np / 128);
     if (form == kQ8 && !ec)
-        return tiles > num_sms;
+        return tiles > num_sms || (2 * tiles > num_sms && (M + 127) / 128 <= pk.Np / 128);
     return 2 * tiles + (ec ? tc_prepass2_room(pk, M, num_sms) : 0) > num_sms;
 }
 
