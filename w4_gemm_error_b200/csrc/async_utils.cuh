@@ -38,15 +38,32 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
-// Arrive, with the release semantics that an arrival has by default: every earlier
-// load and store of this thread, and of the threads that it has met in a barrier
-// since (__syncwarp), is performed before a waiter sees the phase complete.  So a
-// lane that arrives after __syncwarp releases what its whole warp has read, and
-// the copy that the waiter then issues cannot overwrite it too early; that the
-// values' arithmetic may come later does not matter, since they are in registers.
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Orders this thread's ordinary accesses of shared memory against copies (TMA) and
+// tensor-core reads of it, which take another path to it (the async proxy).
+__device__ __forceinline__ void fence_proxy_async_smem()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// A warp gives back a stage that it has read with ordinary loads and that the next
+// copy overwrites.  The arrival's release orders ordinary accesses alone, not the
+// loads against the copy: without the fence the last loads of a stage were
+// performed after the copy behind it had landed (25 to 32 tokens of a 4096 x 14336
+// layer: in every call some warps' 16 channels of the last 8 tokens wrong by half
+// their size; whether it happens depends on how the compiler schedules the loop).
+// The fence costs 0 to 4 % of a decode kernel's time, a vote on the loaded values,
+// which works too, 5 to 8 %.
+__device__ __forceinline__ void release_stage(uint32_t bar, int lane)
+{
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(bar);
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
@@ -230,11 +247,6 @@ __device__ __forceinline__ void bulk_wait_read()
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-__device__ __forceinline__ void fence_proxy_async_smem()
-{
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }

@@ -420,10 +420,7 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                     }
                 }
             }
-            // every lane's shared-memory reads of this stage are done: release it
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_empty + 8 * s);
+            release_stage(bar_empty + 8 * s, lane);
             if (++s == S) {
                 s = 0;
                 par ^= 1u;
@@ -477,9 +474,7 @@ decode_w4ec_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_co
                                        ha[2 * q + 1], xa[2 * q], xa[2 * q + 1]);
                 }
             }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_empty + 8 * s);
+            release_stage(bar_empty + 8 * s, lane);
             if (++s == S) {
                 s = 0;
                 par ^= 1u;

@@ -311,6 +311,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_
                         }
                     }
                 }
+                fence_proxy_async_smem();   // (see release_stage)
                 __syncwarp();
                 // the slot is free: the next unit that uses it
                 if (lane == 0 && i + p.g_slots < n_units) {
@@ -495,9 +496,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&empty[slot]));
+                release_stage(smem_addr(&empty[slot]), lane);
             }
             // ---- group done: partials red[sb][tl][n][row][8 tokens], then the sum
             // over sb pushed to the owning rank

@@ -370,9 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) stack_decode_kernel(StackParams p
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&empty[s]));
+                release_stage(smem_addr(&empty[s]), lane);
                 ++rseq;
                 // partial [16 rows][TOK] of the four warps, summed in warp order
                 if (warp < 4) {
@@ -491,9 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) stack_decode_kernel(StackParams p
                                             }
                                         }
                                     }
-                                    __syncwarp();
-                                    if (lane == 0)
-                                        mbar_arrive(smem_addr(&empty[s]));
+                                    release_stage(smem_addr(&empty[s]), lane);
                                     ++rseq;
                                 }
                             }
@@ -602,7 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1) stack_decode_kernel(StackParams p
                         }
                     }
                 }
-                // the group's operands, partial tiles and outputs are no longer read
+                // the group's operands, partial tiles and outputs are no longer read (the
+                // operands' next copies come after these loads: see release_stage)
+                fence_proxy_async_smem();
                 bar_consumers();
                 if (tid == 0)
                     for (int tg = 0; tg < ng; ++tg)
