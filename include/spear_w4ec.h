@@ -83,7 +83,8 @@ typedef struct spear_w4ec_opts {
 /* Create a layer of K input features, N output features and EC rank r.
  * K and N must be positive multiples of 8; 0 <= r <= 128 (r = 0: no EC).
  * Allocates the packed weights and the workspace on the device (about
- * N*K/2 bytes of codes plus small buffers); no data is packed yet.
+ * N*K/2 bytes of codes plus small buffers, and max_M (K + 8) bytes for
+ * spear_w4ec_forward_q8 where K is no multiple of 16); no data is packed yet.
  * opts may be NULL.  On success *out receives the handle. */
 int spear_w4ec_create(spear_w4ec **out, int64_t K, int64_t N, int32_t r,
                       const spear_w4ec_opts *opts);
@@ -162,14 +163,15 @@ typedef struct spear_w4ec_epilogue {
     int32_t reserved;      /* 0 */
 } spear_w4ec_epilogue;
 
-/* spear_w4ec_forward with an epilogue (ep = NULL: none, the result then equals
- * spear_w4ec_forward's with SPEAR_FORCE_FUSED).  mul and residual may each be
+/* spear_w4ec_forward with an epilogue.  mul and residual may each be
  * y itself (in-place residual addition); every other overlap of y with an
  * operand is SPEAR_ERR_INVALID.  flags: as spear_w4ec_forward, except that the
  * EC is always formed in the kernel of the product (SPEAR_FORCE_SPLIT is
  * SPEAR_ERR_UNSUPPORTED) and the dispatch table, whose times are of the forward
  * without an epilogue, is not used: without a path flag the decode kernels run
- * up to 16 tokens and the tcgen05 kernels beyond. */
+ * up to 16 tokens and the tcgen05 kernels beyond.  An epilogue that does nothing
+ * (ep = NULL, or all its terms NULL with SPEAR_ACT_NONE) is spear_w4ec_forward
+ * with SPEAR_FORCE_FUSED: its kernels, its table, its bits. */
 int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M, const spear_w4ec_epilogue *ep,
                           uint32_t flags, void *stream);
 
@@ -177,8 +179,10 @@ int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M
  *   xq  dev e4m3 [M][K] (4 exponent bits of bias 7, 3 mantissa bits, no
  *       infinities, 0x7F and 0xFF NaN), 16-byte aligned
  *   xs  dev float [M]: one scale a token
- * The products x (q - z) are exact and summed in fp32; a token with a NaN
- * code, or whose scale is not finite, has NaN or infinite outputs.  ep may be
+ * The products x (q - z) are exact and summed in fp32 (the tcgen05 kernels sum
+ * xq q and xq apart and take z times the second off); any finite scale may be
+ * given; a token with a NaN code, or whose scale is not finite, has NaN or
+ * infinite outputs.  ep may be
  * NULL.  flags: as spear_w4ec_forward_ep (without a path flag the decode kernels
  * run up to 8 tokens, up to 16 on layers of one CTA per 16 weight rows). */
 int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y, int64_t M,
@@ -192,7 +196,8 @@ int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, 
  *   s[t]   = a_t / 448,  q[t,k] = e4m3(v[t,k] * (448 / a_t)),
  *            a_t = max(max_k |v[t,k]|, 2^-100)
  * in fp32, each output rounded once (to nearest even; a row of zeros with
- * eps = 0 is 0 / 0).  (q, s) is what
+ * eps = 0 is 0 / 0; a row whose sum of squares leaves fp32, from magnitudes of
+ * about 1e19 on, is 0).  (q, s) is what
  * spear_w4ec_forward_q8 takes.  A row with an infinity or NaN has a scale that
  * is not finite, or NaN outputs.
  *   x, residual, sum, y   dev bf16 [M][K]   weight  dev bf16 [K]

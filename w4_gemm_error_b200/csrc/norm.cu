@@ -188,7 +188,7 @@ template <bool NORM>
 __device__ __forceinline__ Factors factors(const NormParams &p, float sum, float top)
 {
     Factors f;
-    f.rinv = NORM ? rsqrtf(sum / (float)p.K + p.eps) : 1.0f;   // (2 ulp)
+    f.rinv = NORM ? rsqrtf(sum / (float)p.K + p.eps) : 1.0f;   // (2 ulp: a 2^14th of the bf16 rounding)
     const uint32_t amax = __float_as_uint(top * f.rinv) & 0x7FFFFFFFu;
     f.a = __uint_as_float(max(amax, __float_as_uint(kAmaxFloor)));
     f.inv = kE4m3Max / f.a;

@@ -36,11 +36,12 @@
 // with one elected lane in the asynchronous instructions, so that addresses
 // and descriptors stay in uniform registers (issued from a single-lane branch,
 // the four MMAs of a stage alone cost about 400 cycles).
-// Measured in a chain of calls (with the prepass): 4096 tokens of 4096 x 14336,
+// Measured in a short chain of calls (with the prepass): 4096 tokens of 4096 x 14336,
 // 8 bits, SiLU: 205 us, 2390 TFLOP/s (the tensor pipe 73 % active, clocks at
 // 1.4 GHz under the power limit); 2048 tokens, bf16, times a multiplier: 184 us,
 // 1330 TFLOP/s (82 % active; 448 units on 74 pairs are 6.05 rounds, so that a
-// seventh runs nearly empty).  What bounds it is shared memory: a stage is written
+// seventh runs nearly empty).  In runs of seconds, at the clock that the power limit
+// then leaves: 245 us (2000 TFLOP/s) and 217 us (1130 TFLOP/s).  What bounds it is shared memory: a stage is written
 // by TMA and dequantisers and read by the MMAs, 64 KB or about 512 cycles of its
 // 128 bytes a cycle, beside the epilogue's.
 // Two accumulators of 256 columns in TMEM: the epilogue of a tile overlaps the

@@ -6,7 +6,8 @@
 //   kEpi: v = g D[t,1+j],         g = 1 / (1 + exp(-(D[t,0] + b_g)))
 //   kQ8:  v = 2^-9 g D[t,1+j],    g = 1 / (1 + exp(-(xs[t] D[t,0] + b_g))),
 //         rowc: xs[t] and 2^-9 X_t,  X_t = sum_k xq[t,k]
-//   (v rounded to tf32)
+//   (v rounded to tf32, half a unit of 2^-10: the correction enters the product's
+//   accumulator by tf32 MMAs, and is small beside the product)
 //
 // A cluster of S CTAs takes 128 tokens; CTA q the 64-k blocks q, q + S, ...
 // The tokens are the 128 rows (TMEM lanes) of the MMA and the rows of G its N.
