@@ -100,12 +100,15 @@ uint32_t default_path(const spear_w4ec *h, int64_t M)
 // Path of the forms kEpi and kQ8 (the table's times are of the plain kernels,
 // whose tcgen05 family is another one).  Measured in us per call, chained,
 // decode against tcgen05 (bf16 / 8 bits):
-//   4096 x 4096, r 32 (row-CTA kernel)   16 tokens  8.1 / 10.3 against 13.1 / 12.3
-//                                        24 tokens 19.0 / 18.6 against 13.1 / 12.4
-//   4096 x 14336, r 64 (split-K kernel)   8 tokens 14.9 / 16.3 against 22.5 / 18.6
-//                                        16 tokens 20.2 / 21.1 against 23.0 / 19.1
-//                                        24 tokens 31.2 / 32.8 against 23.2 / 19.4
-//   14336 x 4096, r 64 (split-K kernel)  16 tokens 23.5 / 24.0 against 26.6 / 22.3
+//   4096 x 4096, r 32 (row-CTA kernel)   16 tokens  8.2 / 10.3 against 13.0 / 12.2
+//                                        24 tokens 18.9 / 18.9 against 13.1 / 12.3
+//   4096 x 14336, r 64 (split-K kernel)   8 tokens 15.2 / 16.7 against 22.3 / 18.1
+//                                        16 tokens 20.2 / 21.5 against 22.7 / 18.6
+//                                        24 tokens 31.2 / 33.0 against 23.1 / 19.0
+//   14336 x 4096, r 64 (split-K kernel)   8 tokens 18.4 / 17.6 against 26.0 / 21.4
+//                                        16 tokens 24.0 / 24.2 against 26.3 / 21.8
+//   1032 x 2744, r 8 (split-K kernel)     8 tokens  7.1 /  8.3 against  8.5 / 11.1
+//                                        16 tokens 10.4 / 11.7 against  8.8 / 11.5
 // so: the decode kernels up to 16 tokens, but with 8 bits only up to 8 where
 // the row-CTA kernel does not run.
 uint32_t form_path(const spear_w4ec *h, int64_t M, int form)
