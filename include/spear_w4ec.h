@@ -180,9 +180,9 @@ int spear_w4ec_forward_ep(const spear_w4ec *h, const void *x, void *y, int64_t M
  *       infinities, 0x7F and 0xFF NaN), 16-byte aligned
  *   xs  dev float [M]: one scale a token
  * The products x (q - z) are exact and summed in fp32 (the tcgen05 kernels sum
- * xq q and xq apart and take z times the second off); any finite scale may be
- * given; a token with a NaN code, or whose scale is not finite, has NaN or
- * infinite outputs.  ep may be
+ * xq q and xq apart and take z times the second off).  xs may be any finite value
+ * whose product with the layer's scales is finite; a token with a NaN code, or
+ * whose scale is not finite, has NaN or infinite outputs.  ep may be
  * NULL.  flags: as spear_w4ec_forward_ep (without a path flag the decode kernels
  * run up to 8 tokens, up to 16 on layers of one CTA per 16 weight rows). */
 int spear_w4ec_forward_q8(const spear_w4ec *h, const void *xq, const float *xs, void *y, int64_t M,
