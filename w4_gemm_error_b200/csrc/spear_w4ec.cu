@@ -110,7 +110,8 @@ uint32_t default_path(const spear_w4ec *h, int64_t M)
 //   1032 x 2744, r 8 (split-K kernel)     8 tokens  7.1 /  8.3 against  8.5 / 11.1
 //                                        16 tokens 10.4 / 11.7 against  8.8 / 11.5
 // so: the decode kernels up to 16 tokens, but with 8 bits only up to 8 where
-// the row-CTA kernel does not run.
+// the row-CTA kernel does not run (bf16 on narrow layers that it does not take
+// loses up to 1.6 us from 9 to 16 tokens).
 uint32_t form_path(const spear_w4ec *h, int64_t M, int form)
 {
     int64_t most = 16;
